@@ -75,6 +75,20 @@ def lib() -> ctypes.CDLL:
             L.kivi_decode_multi_attn.restype = I32
             L.kivi_decode_multi_workspace_bytes.argtypes = [CFG, I32, I32, I32]
             L.kivi_decode_multi_workspace_bytes.restype = ctypes.c_size_t
+            L.kivi_decode_window_attn.argtypes = [CFG, I32, P, P, P, P, ctypes.c_float, I32, I32, I32, P,
+                                                  ctypes.c_size_t, P, P]
+            L.kivi_decode_window_attn.restype = I32
+            L.kivi_decode_ext_workspace_bytes.argtypes = [CFG, I32, I32]
+            L.kivi_decode_ext_workspace_bytes.restype = ctypes.c_size_t
+            L.kivi_decode_attn_weights.argtypes = [CFG, I32, P, P, P, P, P, P, I32, ctypes.c_float, ctypes.c_float, I32,
+                                                   P, ctypes.c_size_t, P, ctypes.c_size_t, P, P]
+            L.kivi_decode_attn_weights.restype = I32
+            L.kivi_decode_weights_scratch_bytes.argtypes = [CFG, I32, I32]
+            L.kivi_decode_weights_scratch_bytes.restype = ctypes.c_size_t
+            L.kivi_evict_groups.argtypes = [CFG, I32, P, P, P, I32, I32, I32, I32, P, ctypes.c_size_t, P, P]
+            L.kivi_evict_groups.restype = I32
+            L.kivi_evict_scratch_bytes.argtypes = [I32, I32]
+            L.kivi_evict_scratch_bytes.restype = ctypes.c_size_t
             L.kivi_seq_buffer_bytes.argtypes = [CFG, I32, ctypes.POINTER(ctypes.c_size_t)]
             L.kivi_seq_buffer_bytes.restype = I32
             L.kivi_seq_bytes.argtypes = [CFG, I32]
@@ -116,6 +130,19 @@ def _require_cuda(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _require(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torch.device) -> None:
+    """A contiguous tensor of this shape and type on this device (a device without an index is any)."""
+    _require_cuda(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if device.index is not None and t.device.index != device.index:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
 
 
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
@@ -178,6 +205,12 @@ class Config:
 
     def decode_multi_workspace_bytes(self, nseq: int, n_query: int, max_kv_len: int) -> int:
         return int(lib().kivi_decode_multi_workspace_bytes(self.c(), nseq, n_query, max_kv_len))
+
+    def decode_ext_workspace_bytes(self, nseq: int, max_kv_len: int) -> int:
+        return int(lib().kivi_decode_ext_workspace_bytes(self.c(), nseq, max_kv_len))
+
+    def decode_weights_scratch_bytes(self, nseq: int, max_kv_len: int) -> int:
+        return int(lib().kivi_decode_weights_scratch_bytes(self.c(), nseq, max_kv_len))
 
 
 # ---------------------------------------------------------------- codec
@@ -245,17 +278,62 @@ class KVCache:
         self.k_res = torch.zeros((nseq, H, cfg.ring, D), dtype=cfg.torch_dtype, device=dev)
         self.v_res = torch.zeros_like(self.k_res)
         self.kv_len = torch.zeros(nseq, dtype=torch.int32, device=dev)
+        self._finish(0)
+
+    @classmethod
+    def from_buffers(cls, cfg: Config, buffers: dict, kv_len: torch.Tensor, cap_tokens: int,
+                     block_tables: torch.Tensor | None = None, max_len: int | None = None) -> "KVCache":
+        """A cache over buffers that the caller owns (a serving program's pools): `buffers` holds the
+        tensors named in SEQ_FIELDS, kv_len [nseq] int32 the tokens held. Contiguous: packed buffers
+        [nseq][Hkv][...] as kivi.h lays them out for cap_tokens; paged (block_tables [nseq][cap_tokens/G]
+        int32 given): [pages][Hkv][...]. Scales and zeros are int16 or float16 tensors. Nothing is
+        copied: the cache reads and writes these tensors. max_len: host upper bound on every kv_len
+        (default: all that a sequence can hold)."""
+        if cap_tokens % cfg.group:
+            raise ValueError("cap_tokens must be a multiple of G")
+        _require_cuda(kv_len, "kv_len")
+        self = cls.__new__(cls)
+        nseq = int(kv_len.shape[0])
+        self.cfg, self.nseq, self.cap, self.paged = cfg, nseq, cap_tokens, block_tables is not None
+        self.device = kv_len.device
+        H, D, G = cfg.num_kv_heads, cfg.head_dim, cfg.group
+        _require(kv_len, "kv_len", (nseq,), torch.int32, self.device)
+        if self.paged:
+            _require(block_tables, "block_tables", (nseq, cap_tokens // G), torch.int32, self.device)
+            lead, groups, rows = (int(buffers["k_codes"].shape[0]), H), (), (G,)
+        else:
+            lead, groups, rows = (nseq, H), (cap_tokens // G,), (cap_tokens,)
+        shapes = {"k_codes": lead + rows + (cfg.k_row_bytes,), "v_codes": lead + rows + (cfg.v_row_bytes,),
+                  "k_scale": lead + groups + (D,), "k_zero": lead + groups + (D,),
+                  "v_scale": lead + rows + (D // G,), "v_zero": lead + rows + (D // G,),
+                  "k_res": (nseq, H, cfg.ring, D), "v_res": (nseq, H, cfg.ring, D)}
+        for name in SEQ_FIELDS:
+            t = buffers[name]
+            dt = torch.uint8 if name.endswith("codes") else cfg.torch_dtype if name.endswith("res") else torch.int16
+            if dt == torch.int16 and t.dtype == torch.float16:
+                t = t.view(torch.int16)
+            _require(t, name, shapes[name], dt, self.device)
+            setattr(self, name, t)
+        self.kv_len, self.block_tables = kv_len, block_tables
+        self._finish(self.max_tokens if max_len is None else min(int(max_len), self.max_tokens))
+        return self
+
+    def _finish(self, max_len: int) -> None:
+        """The state every cache has beside its buffers: the device array of kivi_seq records."""
+        cfg, nseq, dev = self.cfg, self.nseq, self.device
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.max_len = 0            # host upper bound on every kv_len
+        self.max_len = max_len      # host upper bound on every kv_len
         self._ws = None
+        self._scratch = None
+        self._old = []
         rec = np.zeros((nseq, SEQ_STRUCT_BYTES // 8), dtype=np.uint64)
         for b in range(nseq):
             for i, name in enumerate(SEQ_FIELDS):
                 t = getattr(self, name)
-                rec[b, i] = t.data_ptr() if (paged and name not in ("k_res", "v_res")) else t[b].data_ptr()
+                rec[b, i] = t.data_ptr() if (self.paged and name not in ("k_res", "v_res")) else t[b].data_ptr()
             # cap_tokens (low half), flags (high half); then the block table pointer
-            rec[b, 8] = np.uint64(cap_tokens) | (np.uint64(SEQ_PAGED if paged else 0) << np.uint64(32))
-            rec[b, 9] = np.uint64(self.block_tables[b].data_ptr()) if paged else np.uint64(0)
+            rec[b, 8] = np.uint64(self.cap) | (np.uint64(SEQ_PAGED if self.paged else 0) << np.uint64(32))
+            rec[b, 9] = np.uint64(self.block_tables[b].data_ptr()) if self.paged else np.uint64(0)
         self.seqs = torch.from_numpy(rec.view(np.uint8).reshape(-1)).to(dev)
 
     @property
@@ -334,6 +412,101 @@ class KVCache:
                                             _ptr(out), float(scale), int(mkl), _ptr(ws), ws.numel(),
                                             _ptr(self.status), _stream(self.device)), "kivi_decode_multi_attn")
         return out
+
+    # -------------------------------------------------------------- windows, weights, eviction
+    def _grown(self, old: torch.Tensor | None, need: int, make) -> torch.Tensor:
+        """`old` or a larger buffer. The smaller one stays alive: a captured graph may name it. A buffer
+        made while a stream captures would be filled at replay only, so the call before the
+        capture has to make it."""
+        if old is not None and old.numel() >= need:
+            return old
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the workspace of this call is made by a first call of its size before the capture")
+        if old is not None:
+            self._old.append(old)
+        return make(max(need, 256), dtype=torch.uint8, device=self.device)
+
+    def _zeroed(self, need: int) -> torch.Tensor:
+        """The workspace that every attention call leaves zero-filled, at least `need` bytes."""
+        self._ws = self._grown(self._ws, need, torch.zeros)
+        return self._ws
+
+    def _any(self, need: int) -> torch.Tensor:
+        """Scratch of any contents, at least `need` bytes."""
+        self._scratch = self._grown(self._scratch, need, torch.empty)
+        return self._scratch
+
+    def _decode_args(self, q, out, softmax_scale, max_kv_len):
+        cfg = self.cfg
+        shape = (self.nseq, cfg.num_q_heads, cfg.head_dim)
+        _require(q, "q", shape, cfg.torch_dtype, self.device)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+        else:
+            _require(out, "out", shape, torch.float32, self.device)
+        scale = 1.0 / cfg.head_dim ** 0.5 if softmax_scale is None else softmax_scale
+        return out, float(scale), int(self.max_len if max_kv_len is None else max_kv_len)
+
+    def decode_window(self, q: torch.Tensor, window: int, sinks: int = 0, out: torch.Tensor | None = None,
+                      softmax_scale: float | None = None, max_kv_len: int | None = None) -> torch.Tensor:
+        """Decode attention over the newest `window` tokens and the first `sinks` ones (window 0: all
+        tokens). q [nseq][Hq][D] (cfg dtype) -> out [nseq][Hq][D] fp32."""
+        out, scale, mkl = self._decode_args(q, out, softmax_scale, max_kv_len)
+        cfg = self.cfg
+        with torch.cuda.device(q.device):
+            ws = self._zeroed(cfg.decode_ext_workspace_bytes(self.nseq, mkl))
+            _check(lib().kivi_decode_window_attn(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
+                                                 _ptr(out), scale, int(window), int(sinks), mkl, _ptr(ws), ws.numel(),
+                                                 _ptr(self.status), _stream(q.device)), "kivi_decode_window_attn")
+        return out
+
+    def weight_groups(self) -> int:
+        """Groups per row that hold the weights of any length this cache can reach."""
+        return -(-self.max_tokens // self.cfg.group)
+
+    def decode_weights(self, q: torch.Tensor, weights_in: torch.Tensor | None, weights_out: torch.Tensor | None = None,
+                       decay: float = 1.0, out: torch.Tensor | None = None, softmax_scale: float | None = None,
+                       max_kv_len: int | None = None):
+        """Decode attention that also collects the attention weight of each G-token group:
+        weights_out[b][j] = decay * weights_in[b][j] + the weight all query heads gave to group j. weights_in
+        [nseq][groups] fp32 (None: zeros); weights_out defaults to weights_in, in place. Returns (out, weights_out)."""
+        out, scale, mkl = self._decode_args(q, out, softmax_scale, max_kv_len)
+        cfg = self.cfg
+        given = weights_in if weights_out is None else weights_out
+        if given is None:
+            given = torch.empty((self.nseq, self.weight_groups()), dtype=torch.float32, device=q.device)
+        if given.dim() != 2:
+            raise ValueError("weights must be [nseq][groups]")
+        weights_out, stride = given, int(given.shape[1])
+        _require(weights_out, "weights_out", (self.nseq, stride), torch.float32, self.device)
+        if weights_in is not None:
+            _require(weights_in, "weights_in", (self.nseq, stride), torch.float32, self.device)
+        with torch.cuda.device(q.device):
+            ws = self._zeroed(cfg.decode_ext_workspace_bytes(self.nseq, mkl))
+            sc = self._any(cfg.decode_weights_scratch_bytes(self.nseq, mkl))
+            _check(lib().kivi_decode_attn_weights(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
+                                                  _ptr(out), _ptr(weights_in), _ptr(weights_out), stride, float(decay),
+                                                  scale, mkl, _ptr(ws), ws.numel(), _ptr(sc), sc.numel(),
+                                                  _ptr(self.status), _stream(q.device)), "kivi_decode_attn_weights")
+        return out, weights_out
+
+    def evict(self, weights: torch.Tensor, keep_groups: int, sink_groups: int = 0, recent_groups: int = 0) -> None:
+        """Cut every sequence to its keep_groups packed groups of largest weight (the first
+        sink_groups and the last recent_groups always stay), in place: kv_len, rings, weights
+        [nseq][groups] and the packed buffers or block tables are closed up."""
+        cfg = self.cfg
+        if weights.dim() != 2:
+            raise ValueError("weights must be [nseq][groups]")
+        stride = int(weights.shape[1])
+        _require(weights, "weights", (self.nseq, stride), torch.float32, self.device)
+        if stride * cfg.group < self.max_len:
+            raise ValueError(f"weights must have a column for each of {-(-self.max_len // cfg.group)} groups")
+        with torch.cuda.device(weights.device):
+            sc = self._any(int(lib().kivi_evict_scratch_bytes(self.nseq, stride)))
+            _check(lib().kivi_evict_groups(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(weights),
+                                           stride, int(keep_groups), int(sink_groups), int(recent_groups), _ptr(sc),
+                                           sc.numel(), _ptr(self.status), _stream(weights.device)), "kivi_evict_groups")
+        self.max_len = min(self.max_len, keep_groups * cfg.group + cfg.ring - 1)
 
     # -------------------------------------------------------------- inspection
     def seq_numpy(self, b: int) -> dict:

@@ -213,6 +213,156 @@ kivi_status kivi_decode_multi_attn(const kivi_cfg* cfg, int32_t nseq, const kivi
     return from_cuda(multi_is_decode(cfg, n_query) ? kivi::launch_decode(a, st) : kivi::launch_multi(a, st));
 }
 
+size_t kivi_decode_ext_workspace_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_kv_len) {
+    if (!cfg_ok(cfg) || nseq < 0 || max_kv_len < 0) return 0;
+    const int g = cfg->num_q_heads / cfg->num_kv_heads;
+    size_t cb, pb;
+    kivi::mma_plan(nseq, cfg->num_kv_heads, cfg->head_dim, kivi::ext_heads(g), kivi::ext_parts(g), &cb, &pb);
+    return cb + pb;
+}
+
+// 32-token tiles of the longest sequence, and the scratch bytes of their statistics and of
+// the heads' log sums.
+static size_t weight_tiles(int32_t max_kv_len) { return (static_cast<size_t>(max_kv_len) + kivi::kTile - 1) / kivi::kTile; }
+
+size_t kivi_decode_weights_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_kv_len) {
+    if (!cfg_ok(cfg) || nseq < 0 || max_kv_len < 0) return 0;
+    const size_t heads = static_cast<size_t>(nseq) * cfg->num_q_heads;
+    return heads * weight_tiles(max_kv_len) * sizeof(float2) + heads * sizeof(float);
+}
+
+// Arguments and checks shared by the two extended decode calls.
+static kivi_status ext_args(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs, const int32_t* kv_len,
+                            const void* q, float* out, float softmax_scale, int32_t max_kv_len, void* ws,
+                            size_t ws_bytes, int32_t* status, kivi::DecodeArgs* a) {
+    if (!cfg_ok(cfg)) return KIVI_ERR_ARG;
+    if (nseq < 0 || nseq > 65535 || max_kv_len < 0 || !isfinite(softmax_scale)) return KIVI_ERR_ARG;
+    const int g = cfg->num_q_heads / cfg->num_kv_heads;
+    if (cfg->head_dim != 128 || g > 32) return KIVI_ERR_UNSUPPORTED;
+    if (nseq == 0) return KIVI_OK;
+    if (seqs == nullptr || kv_len == nullptr || q == nullptr || out == nullptr) return KIVI_ERR_ARG;
+    size_t cb, pb;
+    kivi::mma_plan(nseq, cfg->num_kv_heads, cfg->head_dim, kivi::ext_heads(g), kivi::ext_parts(g), &cb, &pb);
+    if (ws == nullptr || ws_bytes < cb + pb) return KIVI_ERR_WORKSPACE;
+    a->chunk = a->max_splits = 0;
+    a->kb = cfg->k_bits;
+    a->vb = cfg->v_bits;
+    a->G = cfg->group;
+    a->D = cfg->head_dim;
+    a->R = cfg->residual;
+    a->Hq = cfg->num_q_heads;
+    a->H = cfg->num_kv_heads;
+    a->dtype = cfg->dtype;
+    a->nseq = nseq;
+    a->max_kv_len = max_kv_len;
+    a->n_query = 0;
+    a->n_part = kivi::ext_parts(g);
+    a->seqs = seqs;
+    a->kv_len = kv_len;
+    a->q = q;
+    a->out = out;
+    a->scale_log2 = softmax_scale * 1.4426950408889634f;
+    a->counters = static_cast<int32_t*>(ws);
+    a->partials = reinterpret_cast<float*>(static_cast<char*>(ws) + cb);
+    a->status = status;
+    return KIVI_OK;
+}
+
+kivi_status kivi_decode_window_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev,
+                                    const int32_t* kv_len_dev, const void* q_dev, float* out_dev,
+                                    float softmax_scale, int32_t window, int32_t sinks, int32_t max_kv_len,
+                                    void* workspace_dev, size_t workspace_bytes, int32_t* status_dev,
+                                    void* stream) {
+    if (window < 0 || sinks < 0) return KIVI_ERR_ARG;
+    kivi::DecodeArgs a;
+    const kivi_status st = ext_args(cfg, nseq, seqs_dev, kv_len_dev, q_dev, out_dev, softmax_scale, max_kv_len,
+                                    workspace_dev, workspace_bytes, status_dev, &a);
+    if (st != KIVI_OK || nseq == 0) return st;
+    a.window = window;
+    a.sinks = sinks;
+    return from_cuda(kivi::launch_ext(a, static_cast<cudaStream_t>(stream)));
+}
+
+kivi_status kivi_decode_attn_weights(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev,
+                                     const int32_t* kv_len_dev, const void* q_dev, float* out_dev,
+                                     const float* weights_in_dev, float* weights_out_dev, int32_t weights_stride,
+                                     float decay, float softmax_scale, int32_t max_kv_len, void* workspace_dev,
+                                     size_t workspace_bytes, void* scratch_dev, size_t scratch_bytes,
+                                     int32_t* status_dev, void* stream) {
+    kivi::DecodeArgs a;
+    if (!cfg_ok(cfg) || weights_stride < 0 || !isfinite(decay)) return KIVI_ERR_ARG;
+    if (static_cast<int64_t>(weights_stride) * cfg->group < max_kv_len) return KIVI_ERR_ARG;
+    const kivi_status st = ext_args(cfg, nseq, seqs_dev, kv_len_dev, q_dev, out_dev, softmax_scale, max_kv_len,
+                                    workspace_dev, workspace_bytes, status_dev, &a);
+    if (st != KIVI_OK || nseq == 0) return st;
+    if (weights_out_dev == nullptr && weights_stride > 0) return KIVI_ERR_ARG;
+    if (scratch_dev == nullptr || scratch_bytes < kivi_decode_weights_scratch_bytes(cfg, nseq, max_kv_len))
+        return KIVI_ERR_WORKSPACE;
+    a.max_tiles = static_cast<int>(weight_tiles(max_kv_len));
+    a.stats = static_cast<float2*>(scratch_dev);
+    a.lse = reinterpret_cast<float*>(a.stats + static_cast<size_t>(nseq) * a.max_tiles * a.Hq);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = kivi::launch_ext(a, s);
+    if (e != cudaSuccess || weights_stride == 0) return from_cuda(e);
+    kivi::GroupWeightArgs w;
+    w.G = a.G;
+    w.R = a.R;
+    w.Hq = a.Hq;
+    w.nseq = nseq;
+    w.max_kv_len = max_kv_len;
+    w.max_tiles = a.max_tiles;
+    w.stride = weights_stride;
+    w.seqs = seqs_dev;
+    w.kv_len = kv_len_dev;
+    w.stats = a.stats;
+    w.lse = a.lse;
+    w.in = weights_in_dev;
+    w.out = weights_out_dev;
+    w.decay = decay;
+    return from_cuda(kivi::launch_group_weights(w, s));
+}
+
+size_t kivi_evict_scratch_bytes(int32_t nseq, int32_t weights_stride) {
+    if (nseq < 0 || weights_stride < 0) return 0;
+    return static_cast<size_t>(nseq) * (static_cast<size_t>(weights_stride) + 2) * sizeof(int32_t);
+}
+
+kivi_status kivi_evict_groups(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev, int32_t* kv_len_dev,
+                              float* weights_dev, int32_t weights_stride, int32_t keep_groups, int32_t sink_groups,
+                              int32_t recent_groups, void* scratch_dev, size_t scratch_bytes, int32_t* status_dev,
+                              void* stream) {
+    if (!cfg_ok(cfg)) return KIVI_ERR_ARG;
+    if (nseq < 0 || nseq > 65535 || weights_stride < 0 || keep_groups < 0 || sink_groups < 0 || recent_groups < 0)
+        return KIVI_ERR_ARG;
+    if (static_cast<int64_t>(sink_groups) + recent_groups > keep_groups) return KIVI_ERR_ARG;
+    if (static_cast<int64_t>(cfg->residual) + cfg->group > kivi::kMaxTurnRing) return KIVI_ERR_UNSUPPORTED;
+    if (nseq == 0) return KIVI_OK;
+    if (seqs_dev == nullptr || kv_len_dev == nullptr || status_dev == nullptr ||
+        (weights_dev == nullptr && weights_stride > 0))
+        return KIVI_ERR_ARG;
+    if (scratch_dev == nullptr || scratch_bytes < kivi_evict_scratch_bytes(nseq, weights_stride))
+        return KIVI_ERR_WORKSPACE;
+    kivi::EvictArgs a;
+    a.kb = cfg->k_bits;
+    a.vb = cfg->v_bits;
+    a.G = cfg->group;
+    a.D = cfg->head_dim;
+    a.R = cfg->residual;
+    a.H = cfg->num_kv_heads;
+    a.nseq = nseq;
+    a.stride = weights_stride;
+    a.keep = keep_groups;
+    a.sink = sink_groups;
+    a.recent = recent_groups;
+    a.seqs = seqs_dev;
+    a.kv_len = kv_len_dev;
+    a.weights = weights_dev;
+    a.cut = static_cast<int32_t*>(scratch_dev);
+    a.map = a.cut + 2 * static_cast<size_t>(nseq);
+    a.status = status_dev;
+    return from_cuda(kivi::launch_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 kivi_status kivi_seq_buffer_bytes(const kivi_cfg* cfg, int32_t cap_tokens, size_t bytes_out[8]) {
     if (!cfg_ok(cfg) || cap_tokens < 0 || cap_tokens % cfg->group != 0 || bytes_out == nullptr) return KIVI_ERR_ARG;
     const size_t H = cfg->num_kv_heads, D = cfg->head_dim, cap = cap_tokens, G = cfg->group;

@@ -53,6 +53,12 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     return a.vb == 2 ? launch_decode_k4v2(a, stream) : launch_decode_k4v4(a, stream);
 }
 
+cudaError_t launch_ext(const DecodeArgs& a, cudaStream_t stream) {
+    if (a.nseq == 0) return cudaSuccess;
+    if (a.kb == 2) return a.vb == 2 ? launch_ext_k2v2(a, stream) : launch_ext_k2v4(a, stream);
+    return a.vb == 2 ? launch_ext_k4v2(a, stream) : launch_ext_k4v4(a, stream);
+}
+
 // Multi-query attention: packed splits of a whole number of 32-token tiles, about an eighth
 // of the longest sequence in 256-token steps between 1024 and 4096 tokens, plus one split
 // for the residual window; one record of kD + 4 floats per (split, virtual head), the

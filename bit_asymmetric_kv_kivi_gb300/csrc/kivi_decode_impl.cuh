@@ -207,18 +207,32 @@ struct CodeShift {
 
 // ---------------------------------------------------------------- lane-layout pieces
 
+// The tokens a windowed query sees: the newest `window` of L (those at lo or later) and the
+// first `sinks`. The default sees everything.
+struct Window {
+    int64_t lo = 0, sinks = 0;
+    __device__ __forceinline__ bool sees(int64_t p) const { return p >= lo || p < sinks; }
+    // whether every token, or any token, of [t, t + kTile) is visible
+    __device__ __forceinline__ bool sees_all(int64_t t) const { return t >= lo || t + kTile <= sinks; }
+    __device__ __forceinline__ bool sees_any(int64_t t) const { return t + kTile > lo || t < sinks; }
+};
+
 // One 32-token tile of residual tokens [ts, min(ts+32, t1)) for one warp, lane = token:
 // scores against the widened stored keys, online-softmax update and value accumulation
 // into the lane-layout state (lane owns channels [4 lane, 4 lane + 4)). Every global
 // load of the tile (the key row, then the lane's value slices of all 32 tokens) is issued
 // before the first use of any, so a tile waits for memory once (for up to four heads; with
 // eight, the value loads follow the scores).
-template <int DT, int GQ>
+// With X (the extended modes) a token is visible only where w sees it (a tile that shows none
+// is left out by the caller) and, when stats is set, the tile's running max and sum of
+// exponentials of head hh go to stats[hh] (hh < nh).
+template <int DT, int GQ, bool X = false>
 __device__ __forceinline__ void residual_tile(const uint16_t* kres, const uint16_t* vres, int ring, int64_t ts,
                                               int64_t t1, const float* qs, int lane, float (&m)[GQ], float (&l)[GQ],
-                                              float (&acc)[GQ][kCpl]) {
+                                              float (&acc)[GQ][kCpl], const Window& w = Window{},
+                                              float2* stats = nullptr, int nh = GQ) {
     const int64_t p = ts + lane;
-    const bool valid = p < t1;
+    const bool valid = p < t1 && (!X || w.sees(p));
     const int ntok = static_cast<int>(t1 - ts < 32 ? t1 - ts : 32);
     const int slot0 = static_cast<int>(ts % ring);
     float sc[GQ];
@@ -261,7 +275,11 @@ __device__ __forceinline__ void residual_tile(const uint16_t* kres, const uint16
         const float mnew = fmaxf(m[hh], tmax);
         const float alpha = exp2f(m[hh] - mnew);
         pr[hh] = valid ? exp2f(sc[hh] - mnew) : 0.0f;
-        l[hh] = l[hh] * alpha + warp_sum(pr[hh]);
+        const float tsum = warp_sum(pr[hh]);
+        l[hh] = l[hh] * alpha + tsum;
+        if constexpr (X) {
+            if (stats != nullptr && lane == 0 && hh < nh) stats[hh] = make_float2(mnew, tsum);
+        }
 #pragma unroll
         for (int c = 0; c < kCpl; ++c) acc[hh][c] *= alpha;
         m[hh] = mnew;
@@ -323,15 +341,24 @@ constexpr int kMinUnitsPerCta = 8;
 constexpr int kMaxCtas = kDecodeMaxCtas;
 constexpr int kMaxDevices = 64;     // devices whose launch sizes are cached
 
+//
+// In the extended modes (MQ == kExtended: a window with sinks, weights per group, any query
+// group) only the tiles with a visible token are units. Listed packed tile i is tile i
+// (i < st: the sinks' tiles) or i + skip (the window's); listed residual tile i is residual
+// tile i + r0.
+constexpr int kExtended = 2;
 struct SeqWork {
     int64_t L, np, ng, rt, u;   // tokens, packed tokens, packed tiles, residual tiles, units
     bool bad;
+    int32_t st, skip, r0;       // extended modes only
+    Window win;
 };
 
-template <int G>
+template <int G, int MQ = 0>
 __device__ __forceinline__ SeqWork seq_work(const DecodeArgs& a, int b) {
     SeqWork w;
     w.L = a.kv_len[b];
+    w.st = w.skip = w.r0 = 0;
     // a.n_query is 0 for decode (an empty sequence gives zeros) and 1 for multi-query
     // attention with one query (kv_len below n_query is a length error)
     w.bad = w.L < a.n_query || w.L > a.max_kv_len || n_packed(w.L, a.R, G) > a.seqs[b].cap_tokens;
@@ -340,6 +367,23 @@ __device__ __forceinline__ SeqWork seq_work(const DecodeArgs& a, int b) {
     w.np = n_packed(w.L, a.R, G);
     w.ng = w.np / kTile;
     w.rt = (w.L - w.np + kTile - 1) / kTile;
+    if constexpr (MQ == kExtended) {
+        if (a.window > 0 && w.L > a.window) {
+            w.win.lo = w.L - a.window;
+            w.win.sinks = a.sinks;
+            const int64_t s = a.sinks < w.np ? a.sinks : w.np, lo = w.win.lo < w.np ? w.win.lo : w.np;
+            const int64_t st = (s + kTile - 1) / kTile, w0 = lo / kTile;
+            if (w0 > st) {
+                w.st = static_cast<int32_t>(st);
+                w.skip = static_cast<int32_t>(w0 - st);
+                w.ng -= w0 - st;
+            }
+            if (w.win.lo > w.np && a.sinks <= w.np) {
+                w.r0 = static_cast<int32_t>((w.win.lo - w.np) / kTile);
+                w.rt -= w.r0;
+            }
+        }
+    }
     w.u = stream_overhead(a) + w.ng + kResidualWeight * w.rt;
     return w;
 }
@@ -373,10 +417,12 @@ __device__ __forceinline__ StreamSegs stream_segs(int64_t s, int64_t Ps, const S
 // synchronized by the caller), then writes the output (the stream's only segment) or the
 // segment's partial record (m, l, acc[kD]) per head at index seg; decode_merge_kernel merges
 // the records of streams with several segments. An empty state (m = -inf, l = 0)
-// contributes nothing.
+// contributes nothing. Only the first nh heads are real (extended modes); lse, when set,
+// takes log2 of each head's sum of exponentials.
 template <int GQ>
 __device__ __forceinline__ void write_segment(const DecodeArgs& a, int nseg, int64_t seg, float* out_s,
-                                              const float* red_m, const float* red_l, const float* red_acc) {
+                                              const float* red_m, const float* red_l, const float* red_acc,
+                                              int nh = GQ, float* lse = nullptr) {
     const int tid = threadIdx.x;
     constexpr int64_t rec = kD + 4;
     for (int i = tid; i < GQ * kD; i += kThreads) {
@@ -394,7 +440,10 @@ __device__ __forceinline__ void write_segment(const DecodeArgs& a, int nseg, int
             }
         }
         if (nseg == 1) {
-            out_s[i] = num / den;
+            if (hh < nh) {
+                out_s[i] = num / den;
+                if (lse != nullptr && d == 0) lse[hh] = M + log2f(den);
+            }
         } else {
             float* r = a.partials + (seg * GQ + hh) * rec;
             r[d] = num;
@@ -420,7 +469,8 @@ __device__ __forceinline__ float* segment_record(const DecodeArgs& a, const Stre
 // log-sum-exp rescaling (a record with a larger max rescales what came before), so the loads
 // of all records are independent of one another.
 template <int GQ>
-__device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSegs& ss, float* out_s) {
+__device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSegs& ss, float* out_s, int nh = GQ,
+                                             float* lse = nullptr) {
     static_assert(kThreads == kD, "one thread per channel");
     const int d = threadIdx.x;
     float M[GQ], den[GQ], num[GQ];
@@ -445,7 +495,12 @@ __device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSe
         }
     }
 #pragma unroll
-    for (int hh = 0; hh < GQ; ++hh) out_s[hh * kD + d] = num[hh] / den[hh];
+    for (int hh = 0; hh < GQ; ++hh) {
+        if (hh < nh) {
+            out_s[hh * kD + d] = num[hh] / den[hh];
+            if (lse != nullptr && d == 0) lse[hh] = M[hh] + log2f(den[hh]);
+        }
+    }
     // the stream's records back to zero (each segment's GQ records are contiguous) once every
     // thread has read them
     __syncthreads();
@@ -462,7 +517,7 @@ struct UnitScan {
     int b_lo, b_hi;
     int64_t mine, start, U;
 };
-template <int G>
+template <int G, int MQ = 0>
 __device__ __forceinline__ UnitScan scan_units(const DecodeArgs& a, int H, int64_t* sched) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     UnitScan us;
@@ -470,7 +525,7 @@ __device__ __forceinline__ UnitScan scan_units(const DecodeArgs& a, int H, int64
     us.b_lo = tid * per < a.nseq ? tid * per : a.nseq;
     us.b_hi = us.b_lo + per < a.nseq ? us.b_lo + per : a.nseq;
     us.mine = 0;
-    for (int b = us.b_lo; b < us.b_hi; ++b) us.mine += static_cast<int64_t>(H) * seq_work<G>(a, b).u;
+    for (int b = us.b_lo; b < us.b_hi; ++b) us.mine += static_cast<int64_t>(H) * seq_work<G, MQ>(a, b).u;
     // within each warp by shuffles, then the four warp totals (a serial scan by one thread
     // cost ~2 us at the start of every launch)
     int64_t incl = us.mine;
@@ -561,32 +616,55 @@ struct MmaSmem {
 // (MQ = 1) QS = n_query and stream h holds the GQ = Hq / Hkv heads of query h % QS. stream_row
 // is the row of the stream's first query head in q and out ([nseq][nq][Hq][D], nq = 1 for
 // decode); stream_query is its query.
+// In the extended modes QS = n_part streams of up to GQ heads hold the Hq / Hkv query heads of a
+// kv head (any query group: 3 heads run as a stream of 4, 5 to 7 as one of 8, more as
+// several of 8); stream_heads is the number of real heads of a stream.
+template <int MQ>
+__device__ __forceinline__ int streams_per_head(const DecodeArgs& a) {
+    return MQ == kExtended ? a.n_part : MQ ? a.n_query : 1;
+}
+template <int GQ, int MQ>
+__device__ __forceinline__ int stream_heads(const DecodeArgs& a, int h) {
+    if constexpr (MQ != kExtended) return GQ;
+    const int left = a.Hq / a.H - (h % a.n_part) * GQ;
+    return left < GQ ? left : GQ;
+}
 template <int GQ, int MQ>
 __device__ __forceinline__ int64_t stream_row(const DecodeArgs& a, int b, int h) {
+    if constexpr (MQ == kExtended)
+        return static_cast<int64_t>(b) * a.Hq + (h / a.n_part) * (a.Hq / a.H) + (h % a.n_part) * GQ;
     if constexpr (!MQ) return static_cast<int64_t>(b) * a.Hq + h * GQ;
     const int nq = a.n_query;
     return (static_cast<int64_t>(b) * nq + h % nq) * a.Hq + (h / nq) * GQ;
 }
 template <int MQ>
 __device__ __forceinline__ int stream_query(const DecodeArgs& a, int h) {
-    if constexpr (!MQ) return 0;
+    if constexpr (MQ != 1) return 0;
     return h % a.n_query;
 }
 
-// q rows [row, row + GQ) into shared memory, scaled by softmax_scale * log2(e); the
+// q rows [row, row + nh) into shared memory (zeros up to GQ), scaled by softmax_scale * log2(e); the
 // caller's earlier use of qs must be over (a CTA barrier) before this runs.
 template <int DT, int GQ>
-__device__ __forceinline__ void load_q(const DecodeArgs& a, float* qs, int64_t row) {
+__device__ __forceinline__ void load_q(const DecodeArgs& a, float* qs, int64_t row, int nh = GQ) {
     const uint16_t* q = static_cast<const uint16_t*>(a.q) + row * kD;
-    for (int i = threadIdx.x; i < GQ * kD; i += kThreads) qs[i] = widen<DT>(q[i]) * a.scale_log2;
+    for (int i = threadIdx.x; i < GQ * kD; i += kThreads) qs[i] = i < nh * kD ? widen<DT>(q[i]) * a.scale_log2 : 0.0f;
+}
+
+// Where the extended modes put a tile's (running max, sum of exponentials): one float2 per
+// (sequence, 32-token tile by position, query head), or null when no weights are wanted.
+__device__ __forceinline__ float2* tile_stats(const DecodeArgs& a, int b, int64_t tile, int head) {
+    return a.stats == nullptr ? nullptr
+                              : a.stats + (static_cast<int64_t>(b) * a.max_tiles + tile) * a.Hq + head;
 }
 
 // Residual tiles [t0, t1) of sequence b, kv head hk (tile i = tokens np + 32 i ..), lane-layout
 // CUDA-core path, over the tokens below lend (w.L, or the causal end of a stream's query);
 // leaves the merged warp states in red_* (synchronized).
-template <int DT, int GQ, int G>
+template <int DT, int GQ, int G, bool X = false>
 __device__ __forceinline__ void residual_segment(const DecodeArgs& a, const MmaSmem& sm, int b, int hk,
-                                                 const SeqWork& w, int64_t lend, int64_t t0, int64_t t1) {
+                                                 const SeqWork& w, int64_t lend, int64_t t0, int64_t t1,
+                                                 int head0 = 0, int nh = GQ) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ring = a.R + G;
     const kivi_seq& sq = a.seqs[b];
     float m[GQ], l[GQ], acc[GQ][kCpl];
@@ -601,6 +679,18 @@ __device__ __forceinline__ void residual_segment(const DecodeArgs& a, const MmaS
     const uint16_t* vres = static_cast<const uint16_t*>(sq.v_res) + static_cast<int64_t>(hk) * ring * kD;
     const int64_t tv = (lend - w.np + kTile - 1) / kTile;   // tiles holding visible tokens
     const int64_t te = t1 < tv ? t1 : tv;
+    if constexpr (X) {
+        for (int64_t i = t0 + w.r0 + warp; i < t1 + w.r0; i += kWarps) {
+            const int64_t ts = w.np + kTile * i;
+            if (w.win.sees_any(ts))
+                residual_tile<DT, GQ, true>(kres, vres, ring, ts, lend, sm.qs, lane, m, l, acc, w.win,
+                                            tile_stats(a, b, ts / kTile, head0), nh);
+            __syncwarp();
+        }
+        store_lane_state<GQ>(warp, lane, m, l, acc, sm.red_m, sm.red_l, sm.red_acc);
+        __syncthreads();
+        return;
+    }
     for (int64_t i = t0 + warp; i < te; i += kWarps) {
         residual_tile<DT, GQ>(kres, vres, ring, w.np + kTile * i, lend, sm.qs, lane, m, l, acc);
         __syncwarp();
@@ -661,9 +751,15 @@ __device__ __forceinline__ void bias_batch(const unsigned char* zb, int gid, int
 // Packed tiles [ga, gb) of sequence b, kv head hk, for the GQ query heads at q row qrow, on
 // the tensor cores; leaves the merged warp states
 // in red_* (synchronized). Issues its first stages, then loads the stream's q into qs.
-template <int KB, int VB, int DT, int GQ, int G>
+//
+// X (extended modes): [ga, gb) are listed tiles (SeqWork), tokens outside the window are masked
+// before the softmax, and the tile's statistics are stored. The value products of one tile
+// go to fresh accumulators that are then added with fp32 adds: the tensor core truncates
+// when it accumulates, and over the hundreds of tiles of a long stream the running output
+// came out up to 8e-5 (relative, 64 x 32768 tokens) short of its sum.
+template <int KB, int VB, int DT, int GQ, int G, bool X = false>
 __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem& sm, int b, int64_t qrow, int hk, int64_t ga,
-                                              int64_t gb) {
+                                              int64_t gb, const SeqWork& sw = SeqWork{}, int head0 = 0, int nh = GQ) {
     using Lay = MmaLayout<KB, VB>;
     constexpr int RBK = Lay::kKRowBytes, RBV = Lay::kVRowBytes;
     constexpr int STAGE = Lay::kStage;
@@ -750,9 +846,12 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
     // page of this warp's i-th tile (paged sequences); the in-loop issue uses an entry
     // loaded one iteration earlier, so the table read stays off the critical path
     const uint32_t gfirst32 = static_cast<uint32_t>(gfirst);
-    auto page_of = [&](int i) -> int32_t {
-        return paged ? sq.block_table[(gfirst32 + kWarps * static_cast<uint32_t>(i)) / TPG] : 0;
+    const uint32_t st32 = static_cast<uint32_t>(sw.st), skip32 = static_cast<uint32_t>(sw.skip);
+    auto tile_of = [&](int i) -> uint32_t {   // this warp's i-th tile
+        const uint32_t j = gfirst32 + kWarps * static_cast<uint32_t>(i);
+        return X && j >= st32 ? j + skip32 : j;
     };
+    auto page_of = [&](int i) -> int32_t { return paged ? sq.block_table[tile_of(i) / TPG] : 0; };
     // key zeros of this warp's tiles [i0, i0 + kZB) (those below n_my) into its buffer: lane L
     // copies chunk L % 16 of rows L / 16, L / 16 + 2, ...
     unsigned char* zb = sm.zbuf + warp * kZB * kZRow;
@@ -762,7 +861,7 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
         for (int m = 0; m < kZB / 2; ++m) {
             const int r = (lane >> 4) + 2 * m, i = i0 + r;
             if (i < n_my) {
-                const uint32_t j = gfirst32 + kWarps * static_cast<uint32_t>(i);
+                const uint32_t j = tile_of(i);
                 const uint32_t kg = paged ? static_cast<uint32_t>(sq.block_table[j / TPG]) * static_cast<uint32_t>(a.H) +
                                                 static_cast<uint32_t>(hk)
                                           : j / TPG;
@@ -773,14 +872,14 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
     issue_z(0);   // joins the first stage's group
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        if (i < n_my) issue(i, gfirst32 + kWarps * i, page_of(i));
+        if (i < n_my) issue(i, tile_of(i), page_of(i));
         cp_async_commit();
     }
     int32_t pg_ahead = kStages - 1 < n_my ? page_of(kStages - 1) : 0;
 
     // q of the stream, loaded while the first stages are in flight (the caller's barrier
     // has ended the previous segment's use of qs and of the stages)
-    load_q<DT, GQ>(a, qs, qrow);
+    load_q<DT, GQ>(a, qs, qrow, nh);
     __syncthreads();
 
     // q prescale: a power of two putting max |q| in (1/2, 1]
@@ -839,7 +938,7 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
         {
             const int nxt = it + kStages - 1;
             if (nxt < n_my) {
-                issue(nxt % kStages, gfirst32 + kWarps * static_cast<uint32_t>(nxt), pg_ahead);
+                issue(nxt % kStages, tile_of(nxt), pg_ahead);
                 pg_ahead = nxt + 1 < n_my ? page_of(nxt + 1) : 0;
             }
             cp_async_commit();
@@ -938,7 +1037,15 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
         // ---- online softmax for head t over tokens gid, gid+8, gid+16, gid+24; the scores are
         // in units of the prescaled q, and qpost (a power of two) scales them exactly inside
         // the max and the exponent
-        const float S[4] = {c0[0] + c0[1], c0[2] + c0[3], c1[0] + c1[1], c1[2] + c1[3]};
+        float S[4] = {c0[0] + c0[1], c0[2] + c0[3], c1[0] + c1[1], c1[2] + c1[3]};
+        if constexpr (X) {   // a listed tile shows at least one token, so the head's max stays finite
+            const int64_t t0 = static_cast<int64_t>(tile_of(it)) * kTile;
+            if (!sw.win.sees_all(t0)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!sw.win.sees(t0 + gid + 8 * r)) S[r] = -CUDART_INF_F;
+            }
+        }
         float tmax = fmaxf(fmaxf(S[0], S[1]), fmaxf(S[2], S[3]));
         const float spost = kCvtK ? qpost * kE4m3Unit : qpost;   // exact: both powers of two
         // the head's max over the tile's 32 tokens (a reduction over the lanes of head t) is
@@ -961,7 +1068,17 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
         float p[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) p[r] = (GQ >= 4 || t < GQ) ? exp2_ftz(fmaf(S[r], spost, -m_run)) : 0.0f;
-        l_run += (p[0] + p[1]) + (p[2] + p[3]);
+        const float psum = (p[0] + p[1]) + (p[2] + p[3]);
+        l_run += psum;
+        if constexpr (X) {
+            if (a.stats != nullptr) {
+                float ts = psum;
+                ts += __shfl_xor_sync(kFull, ts, 4);
+                ts += __shfl_xor_sync(kFull, ts, 8);
+                ts += __shfl_xor_sync(kFull, ts, 16);
+                if (gid == 0 && t < nh) tile_stats(a, b, tile_of(it), head0)[t] = make_float2(m_run, ts);
+            }
+        }
 #pragma unroll
         // token 8r + j goes to column 8r + 2 (j % 4) + j / 4: the value side pairs tokens
         // (8r + t', 8r + t' + 4), which then sit side by side
@@ -1004,32 +1121,51 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
                 za[k2][e] = gid < NVG ? prmt(zw0, zw1, sel_z) : 0u;
             }
         }
+        if constexpr (X) {
+            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) mma_f16(cz, za[k2][0], 0u, za[k2][1], 0u, bp[k2][0], bp[k2][1]);
+            for (int k2 = 0; k2 < 2; ++k2) mma_f16(f, za[k2][0], 0u, za[k2][1], 0u, bp[k2][0], bp[k2][1]);
+            cz[0] += f[0]; cz[1] += f[1];   // rows 8 .. 15 are zero
+        } else {
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) mma_f16(cz, za[k2][0], 0u, za[k2][1], 0u, bp[k2][0], bp[k2][1]);
+        }
 
         // ---- value codes (A = codes^T, rows = channels of one channel group) and P' V
+        auto value_mma = [&](int k2, int kg, float (&u0)[4], float (&u1)[4]) {
+            uint32_t wv[2], wvs[2];
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
+            for (int e = 0; e < 2; ++e) {
+                const int tau0 = 16 * k2 + 8 * e + t;
+                const int off = kg * (RBV / 4) + vbyte;
+                const uint32_t x0 = *reinterpret_cast<const uint32_t*>(vc + tau0 * RBV + off);
+                const uint32_t x1 = *reinterpret_cast<const uint32_t*>(vc + (tau0 + 4) * RBV + off);
+                wv[e] = prmt(x0, x1, sel_v);
+                wvs[e] = wv[e] >> SHIFTV;
+            }
+            // m-tile 2kg + u: rows gid (slot 2u) and gid + 8 (slot 2u + 1)
+            mma_f16(u0, code_pair<VB, 0>(wv[0], wvs[0]), code_pair<VB, 1>(wv[0], wvs[0]),
+                    code_pair<VB, 0>(wv[1], wvs[1]), code_pair<VB, 1>(wv[1], wvs[1]), vb[k2][0][kg], vb[k2][1][kg]);
+            mma_f16(u1, code_pair<VB, 2>(wv[0], wvs[0]), code_pair<VB, 3>(wv[0], wvs[0]),
+                    code_pair<VB, 2>(wv[1], wvs[1]), code_pair<VB, 3>(wv[1], wvs[1]), vb[k2][0][kg], vb[k2][1][kg]);
+        };
+        if constexpr (X) {
 #pragma unroll
             for (int kg = 0; kg < 4; ++kg) {
-                uint32_t wv[2], wvs[2];
+                float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tau0 = 16 * k2 + 8 * e + t;
-                    const int off = kg * (RBV / 4) + vbyte;
-                    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(vc + tau0 * RBV + off);
-                    const uint32_t x1 = *reinterpret_cast<const uint32_t*>(vc + (tau0 + 4) * RBV + off);
-                    wv[e] = prmt(x0, x1, sel_v);
-                    wvs[e] = wv[e] >> SHIFTV;
+                for (int k2 = 0; k2 < 2; ++k2) value_mma(k2, kg, u0, u1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    cv[2 * kg][i] += u0[i];
+                    cv[2 * kg + 1][i] += u1[i];
                 }
-                // m-tile 2kg + u: rows gid (slot 2u) and gid + 8 (slot 2u + 1)
-                mma_f16(cv[2 * kg], code_pair<VB, 0>(wv[0], wvs[0]), code_pair<VB, 1>(wv[0], wvs[0]),
-                        code_pair<VB, 0>(wv[1], wvs[1]), code_pair<VB, 1>(wv[1], wvs[1]), vb[k2][0][kg],
-                        vb[k2][1][kg]);
-                mma_f16(cv[2 * kg + 1], code_pair<VB, 2>(wv[0], wvs[0]), code_pair<VB, 3>(wv[0], wvs[0]),
-                        code_pair<VB, 2>(wv[1], wvs[1]), code_pair<VB, 3>(wv[1], wvs[1]), vb[k2][0][kg],
-                        vb[k2][1][kg]);
             }
+        } else {
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                for (int kg = 0; kg < 4; ++kg) value_mma(k2, kg, cv[2 * kg], cv[2 * kg + 1]);
         }
         __syncwarp();
     }
@@ -1069,9 +1205,10 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
 // instructions for two registers. The kv head's tiles are read once for all eight heads.
 // C columns 2t and 2t + 1 are heads 2t and 2t + 1, so each thread keeps the online softmax
 // of two heads.
-template <int KB, int VB, int DT, int G>
+template <int KB, int VB, int DT, int G, bool X = false>
 __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSmem& sm, int b, int64_t qrow, int hk,
-                                               int64_t ga, int64_t gb) {
+                                               int64_t ga, int64_t gb, const SeqWork& sw = SeqWork{}, int head0 = 0,
+                                               int nh = 8) {
     constexpr int GQ = 8;
     using Lay = MmaLayout<KB, VB>;
     constexpr int RBK = Lay::kKRowBytes, RBV = Lay::kVRowBytes;
@@ -1138,9 +1275,12 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
         if (v_issue) cp_async16(dst + vm_dst, vm_lane + static_cast<uint64_t>(rt) * VMETA);
     };
     const uint32_t gfirst32 = static_cast<uint32_t>(gfirst);
-    auto page_of = [&](int i) -> int32_t {
-        return paged ? sq.block_table[(gfirst32 + kWarps * static_cast<uint32_t>(i)) / TPG] : 0;
+    const uint32_t st32 = static_cast<uint32_t>(sw.st), skip32 = static_cast<uint32_t>(sw.skip);
+    auto tile_of = [&](int i) -> uint32_t {   // this warp's i-th tile
+        const uint32_t j = gfirst32 + kWarps * static_cast<uint32_t>(i);
+        return X && j >= st32 ? j + skip32 : j;
     };
+    auto page_of = [&](int i) -> int32_t { return paged ? sq.block_table[tile_of(i) / TPG] : 0; };
     // key zeros of this warp's tiles [i0, i0 + kZB) (those below n_my) into its buffer: lane L
     // copies chunk L % 16 of rows L / 16, L / 16 + 2, ...
     unsigned char* zb = sm.zbuf + warp * kZB * kZRow;
@@ -1150,7 +1290,7 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
         for (int m = 0; m < kZB / 2; ++m) {
             const int r = (lane >> 4) + 2 * m, i = i0 + r;
             if (i < n_my) {
-                const uint32_t j = gfirst32 + kWarps * static_cast<uint32_t>(i);
+                const uint32_t j = tile_of(i);
                 const uint32_t kg = paged ? static_cast<uint32_t>(sq.block_table[j / TPG]) * static_cast<uint32_t>(a.H) +
                                                 static_cast<uint32_t>(hk)
                                           : j / TPG;
@@ -1161,12 +1301,12 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
     issue_z(0);   // joins the first stage's group
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) {
-        if (i < n_my) issue(i, gfirst32 + kWarps * i, page_of(i));
+        if (i < n_my) issue(i, tile_of(i), page_of(i));
         cp_async_commit();
     }
     int32_t pg_ahead = kStages - 1 < n_my ? page_of(kStages - 1) : 0;
 
-    load_q<DT, GQ>(a, qs, qrow);
+    load_q<DT, GQ>(a, qs, qrow, nh);
     __syncthreads();
     float qmax_abs = 0.0f;
     for (int i = tid; i < GQ * kD; i += kThreads) qmax_abs = fmaxf(qmax_abs, fabsf(qs[i]));
@@ -1205,7 +1345,7 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
         {
             const int nxt = it + kStages - 1;
             if (nxt < n_my) {
-                issue(nxt % kStages, gfirst32 + kWarps * static_cast<uint32_t>(nxt), pg_ahead);
+                issue(nxt % kStages, tile_of(nxt), pg_ahead);
                 pg_ahead = nxt + 1 < n_my ? page_of(nxt + 1) : 0;
             }
             cp_async_commit();
@@ -1289,6 +1429,20 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
             c0[i] += c0o[i];
             c1[i] += c1o[i];
         }
+        if constexpr (X) {
+            const int64_t t0 = static_cast<int64_t>(tile_of(it)) * kTile;
+            if (!sw.win.sees_all(t0)) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {   // rows gid + 8 r of c0 and gid + 16 + 8 r of c1
+                    const bool v0 = sw.win.sees(t0 + gid + 8 * r), v1 = sw.win.sees(t0 + gid + 16 + 8 * r);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (!v0) c0[2 * r + e] = -CUDART_INF_F;
+                        if (!v1) c1[2 * r + e] = -CUDART_INF_F;
+                    }
+                }
+            }
+        }
         float p[2][4];
         bool grow = false;
         float mnew[2];
@@ -1322,7 +1476,18 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
             p[e][1] = exp2_ftz(fmaf(c0[2 + e], qpost, -m_run[e]));
             p[e][2] = exp2_ftz(fmaf(c1[e], qpost, -m_run[e]));
             p[e][3] = exp2_ftz(fmaf(c1[2 + e], qpost, -m_run[e]));
-            l_run[e] += (p[e][0] + p[e][1]) + (p[e][2] + p[e][3]);
+            const float psum = (p[e][0] + p[e][1]) + (p[e][2] + p[e][3]);
+            l_run[e] += psum;
+            if constexpr (X) {
+                if (a.stats != nullptr) {
+                    float ts = psum;
+                    ts += __shfl_xor_sync(kFull, ts, 4);
+                    ts += __shfl_xor_sync(kFull, ts, 8);
+                    ts += __shfl_xor_sync(kFull, ts, 16);
+                    if (gid == 0 && 2 * t + e < nh)
+                        tile_stats(a, b, tile_of(it), head0)[2 * t + e] = make_float2(m_run[e], ts);
+                }
+            }
         }
         // token 8r + j to column 8r + 2 (j % 4) + j / 4, as in group_segment
 #pragma unroll
@@ -1365,36 +1530,55 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
                 za[k2][e] = gid < NVG ? prmt(zw0, zw1, sel_z) : 0u;
             }
         }
+        float fz[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float(&zc)[4] = X ? fz : cz;
 #pragma unroll
         for (int k2 = 0; k2 < 2; ++k2) {
-            mma_f16(cz, za[k2][0], 0u, za[k2][1], 0u, bph[k2][0], bph[k2][1]);
-            mma_f16(cz, za[k2][0], 0u, za[k2][1], 0u, bpl[k2][0], bpl[k2][1]);
+            mma_f16(zc, za[k2][0], 0u, za[k2][1], 0u, bph[k2][0], bph[k2][1]);
+            mma_f16(zc, za[k2][0], 0u, za[k2][1], 0u, bpl[k2][0], bpl[k2][1]);
+        }
+        if constexpr (X) {
+            cz[0] += fz[0]; cz[1] += fz[1];   // rows 8 .. 15 are zero
         }
 
         // value codes (A = codes^T, rows = channels) against hi, then lo
+        auto value_mma = [&](int k2, int kg, float (&u0)[4], float (&u1)[4]) {
+            uint32_t wv[2], wvs[2];
 #pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
+            for (int e = 0; e < 2; ++e) {
+                const int tau0 = 16 * k2 + 8 * e + t;
+                const int off = kg * (RBV / 4) + vbyte;
+                const uint32_t x0 = *reinterpret_cast<const uint32_t*>(vc + tau0 * RBV + off);
+                const uint32_t x1 = *reinterpret_cast<const uint32_t*>(vc + (tau0 + 4) * RBV + off);
+                wv[e] = prmt(x0, x1, sel_v);
+                wvs[e] = wv[e] >> SHIFTV;
+            }
+            const uint32_t a00 = code_pair<VB, 0>(wv[0], wvs[0]), a01 = code_pair<VB, 1>(wv[0], wvs[0]);
+            const uint32_t a02 = code_pair<VB, 0>(wv[1], wvs[1]), a03 = code_pair<VB, 1>(wv[1], wvs[1]);
+            const uint32_t a10 = code_pair<VB, 2>(wv[0], wvs[0]), a11 = code_pair<VB, 3>(wv[0], wvs[0]);
+            const uint32_t a12 = code_pair<VB, 2>(wv[1], wvs[1]), a13 = code_pair<VB, 3>(wv[1], wvs[1]);
+            mma_f16(u0, a00, a01, a02, a03, vbh[k2][0][kg], vbh[k2][1][kg]);
+            mma_f16(u1, a10, a11, a12, a13, vbh[k2][0][kg], vbh[k2][1][kg]);
+            mma_f16(u0, a00, a01, a02, a03, vbl[k2][0][kg], vbl[k2][1][kg]);
+            mma_f16(u1, a10, a11, a12, a13, vbl[k2][0][kg], vbl[k2][1][kg]);
+        };
+        if constexpr (X) {   // fresh accumulators per tile, as in group_segment
 #pragma unroll
             for (int kg = 0; kg < 4; ++kg) {
-                uint32_t wv[2], wvs[2];
+                float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tau0 = 16 * k2 + 8 * e + t;
-                    const int off = kg * (RBV / 4) + vbyte;
-                    const uint32_t x0 = *reinterpret_cast<const uint32_t*>(vc + tau0 * RBV + off);
-                    const uint32_t x1 = *reinterpret_cast<const uint32_t*>(vc + (tau0 + 4) * RBV + off);
-                    wv[e] = prmt(x0, x1, sel_v);
-                    wvs[e] = wv[e] >> SHIFTV;
+                for (int k2 = 0; k2 < 2; ++k2) value_mma(k2, kg, u0, u1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    cv[2 * kg][i] += u0[i];
+                    cv[2 * kg + 1][i] += u1[i];
                 }
-                const uint32_t a00 = code_pair<VB, 0>(wv[0], wvs[0]), a01 = code_pair<VB, 1>(wv[0], wvs[0]);
-                const uint32_t a02 = code_pair<VB, 0>(wv[1], wvs[1]), a03 = code_pair<VB, 1>(wv[1], wvs[1]);
-                const uint32_t a10 = code_pair<VB, 2>(wv[0], wvs[0]), a11 = code_pair<VB, 3>(wv[0], wvs[0]);
-                const uint32_t a12 = code_pair<VB, 2>(wv[1], wvs[1]), a13 = code_pair<VB, 3>(wv[1], wvs[1]);
-                mma_f16(cv[2 * kg], a00, a01, a02, a03, vbh[k2][0][kg], vbh[k2][1][kg]);
-                mma_f16(cv[2 * kg + 1], a10, a11, a12, a13, vbh[k2][0][kg], vbh[k2][1][kg]);
-                mma_f16(cv[2 * kg], a00, a01, a02, a03, vbl[k2][0][kg], vbl[k2][1][kg]);
-                mma_f16(cv[2 * kg + 1], a10, a11, a12, a13, vbl[k2][0][kg], vbl[k2][1][kg]);
             }
+        } else {
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+                for (int kg = 0; kg < 4; ++kg) value_mma(k2, kg, cv[2 * kg], cv[2 * kg + 1]);
         }
         __syncwarp();
     }
@@ -1447,14 +1631,15 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
     asm volatile("griddepcontrol.launch_dependents;");
     // streams: (sequence, h), kv head h / QS: decode has one per kv head (its GQ query heads);
     // several queries (MQ) have one per query and kv head, each reading the kv head
-    const int QS = MQ ? a.n_query : 1;   // streams per kv head
+    constexpr bool X = MQ == kExtended;
+    const int QS = streams_per_head<MQ>(a);   // streams per kv head
     const int C = gridDim.x, c = blockIdx.x, H = a.H * QS;
 
     // sequences without work: zeros for an empty one, NaN and a status for a bad length
     for (int b = c; b < a.nseq; b += C) {
-        const SeqWork w = seq_work<G>(a, b);
+        const SeqWork w = seq_work<G, MQ>(a, b);
         if (w.u != 0) continue;
-        const int rows = a.Hq * QS;
+        const int rows = X ? a.Hq : a.Hq * QS;
         float* o = a.out + static_cast<int64_t>(b) * rows * kD;
         for (int i = tid; i < rows * kD; i += kThreads) o[i] = w.bad ? CUDART_NAN_F : 0.0f;
         if (w.bad && tid == 0) set_status(a.status, KIVI_ERR_LENGTH);
@@ -1468,7 +1653,7 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
     if (tid == 0) vw[5] = a.nseq;
     // units before each thread's run of sequences (exclusive scan), the total U, and this
     // CTA's range [lo, hi)
-    const UnitScan us = scan_units<G>(a, H, sched);
+    const UnitScan us = scan_units<G, MQ>(a, H, sched);
     const int b_lo = us.b_lo, b_hi = us.b_hi;
     const int64_t mine = us.mine, U = us.U;
     const int64_t Ceff = effective_ctas(U, C);
@@ -1478,7 +1663,7 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
     if (mine > 0 && lo >= start && lo < start + mine) {
         int64_t p = start;
         for (int b = b_lo; b < b_hi; ++b) {
-            const int64_t us = seq_work<G>(a, b).u, ub = static_cast<int64_t>(H) * us;
+            const int64_t us = seq_work<G, MQ>(a, b).u, ub = static_cast<int64_t>(H) * us;
             if (lo < p + ub) {
                 vw[0] = lo;
                 vw[1] = hi;
@@ -1505,7 +1690,7 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
         Cur k;
         k.b = static_cast<int>(vw[5]);
         k.h = static_cast<int>(vw[6]);
-        k.w = seq_work<G>(a, k.b);
+        k.w = seq_work<G, MQ>(a, k.b);
         k.Ps = vw[4] + k.h * k.w.u;
         k.Ws = k.Ps + stream_overhead(a);
         const int64_t lo_ = vw[0], hi_ = vw[1];
@@ -1521,7 +1706,12 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
         const int64_t s_ = static_cast<int64_t>(k.b) * H + k.h;
         const StreamSegs ss = stream_segs(s_, k.Ps, k.w, vw[2], vw[3], stream_overhead(a));
         float* out_s = a.out + stream_row<GQ, MQ>(a, k.b, k.h) * kD;
-        write_segment<GQ>(a, ss.nseg, 2 * s_ + part + c, out_s, sm.red_m, sm.red_l, sm.red_acc);
+        if constexpr (X)
+            write_segment<GQ>(a, ss.nseg, 2 * s_ + part + c, out_s, sm.red_m, sm.red_l, sm.red_acc,
+                              stream_heads<GQ, MQ>(a, k.h),
+                              a.lse == nullptr ? nullptr : a.lse + stream_row<GQ, MQ>(a, k.b, k.h));
+        else
+            write_segment<GQ>(a, ss.nseg, 2 * s_ + part + c, out_s, sm.red_m, sm.red_l, sm.red_acc);
     };
 
     while (true) {
@@ -1535,12 +1725,14 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
             bool q_ready = false;   // qs holds this stream's q (loaded by its group segment here)
             if (k.x0 < k.w.ng) {
                 __syncthreads();   // the previous segment is done with qs and the shared arrays
+                const int64_t x1 = k.x1 < k.w.ng ? k.x1 : k.w.ng;
+                const int64_t row = stream_row<GQ, MQ>(a, k.b, k.h);
+                const int nh = stream_heads<GQ, MQ>(a, k.h);
+                const int head0 = X ? static_cast<int>(row - static_cast<int64_t>(k.b) * a.Hq) : 0;
                 if constexpr (GQ == 8)
-                    group_segment8<KB, VB, DT, G>(a, sm, k.b, stream_row<GQ, MQ>(a, k.b, k.h), k.h / QS, k.x0,
-                                                  k.x1 < k.w.ng ? k.x1 : k.w.ng);
+                    group_segment8<KB, VB, DT, G, X>(a, sm, k.b, row, k.h / QS, k.x0, x1, k.w, head0, nh);
                 else
-                    group_segment<KB, VB, DT, GQ, G>(a, sm, k.b, stream_row<GQ, MQ>(a, k.b, k.h), k.h / QS, k.x0,
-                                                     k.x1 < k.w.ng ? k.x1 : k.w.ng);
+                    group_segment<KB, VB, DT, GQ, G, X>(a, sm, k.b, row, k.h / QS, k.x0, x1, k.w, head0, nh);
                 finish(0);
                 k = current();
                 q_ready = true;
@@ -1549,13 +1741,17 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
                 const int64_t u0 = (k.x0 > k.w.ng ? k.x0 : k.w.ng) - k.w.ng, u1 = k.x1 - k.w.ng;
                 __syncthreads();   // the merge arrays and qs are free
                 if (!q_ready) {
-                    load_q<DT, GQ>(a, sm.qs, stream_row<GQ, MQ>(a, k.b, k.h));
+                    load_q<DT, GQ>(a, sm.qs, stream_row<GQ, MQ>(a, k.b, k.h), stream_heads<GQ, MQ>(a, k.h));
                     __syncthreads();
                 }
                 // the stream's query i sees tokens below L - n_query + 1 + i (L for decode)
-                const int64_t lend = k.w.L - (QS - 1 - stream_query<MQ>(a, k.h));
-                residual_segment<DT, GQ, G>(a, sm, k.b, k.h / QS, k.w, lend, (u0 + kResidualWeight - 1) / kResidualWeight,
-                                         (u1 + kResidualWeight - 1) / kResidualWeight);
+                const int64_t lend = X ? k.w.L : k.w.L - (QS - 1 - stream_query<MQ>(a, k.h));
+                const int64_t r0 = (u0 + kResidualWeight - 1) / kResidualWeight;
+                const int64_t r1 = (u1 + kResidualWeight - 1) / kResidualWeight;
+                const int head0 =
+                    X ? static_cast<int>(stream_row<GQ, MQ>(a, k.b, k.h) - static_cast<int64_t>(k.b) * a.Hq) : 0;
+                residual_segment<DT, GQ, G, X>(a, sm, k.b, k.h / QS, k.w, lend, r0, r1, head0,
+                                               stream_heads<GQ, MQ>(a, k.h));
                 finish(1);
             }
         }
@@ -1565,7 +1761,7 @@ __global__ void __launch_bounds__(kThreads, KB + VB <= 6 ? 3 : 2) decode_mma_ker
             if (h + 1 < H) {
                 vw[6] = h + 1;
             } else {
-                vw[4] = vw[4] + static_cast<int64_t>(H) * seq_work<G>(a, b).u;
+                vw[4] = vw[4] + static_cast<int64_t>(H) * seq_work<G, MQ>(a, b).u;
                 vw[5] = b + 1;
                 vw[6] = 0;
             }
@@ -1606,16 +1802,16 @@ template <int GQ, int G, int MQ>
 __global__ void __launch_bounds__(kThreads) decode_merge_kernel(DecodeArgs a, int C) {
     __shared__ int64_t sched[kThreads + 1 + kWarps];
     __shared__ int64_t stream_at[2];   // first unit of the stream, units of one of its sequence's streams
-    const int H = a.H * (MQ ? a.n_query : 1);
-    const UnitScan us = scan_units<G>(a, H, sched);
+    const int H = a.H * streams_per_head<MQ>(a);
+    const UnitScan us = scan_units<G, MQ>(a, H, sched);
     const int64_t Ceff = effective_ctas(us.U, C);
     const int64_t S = us.U == 0 ? 0 : static_cast<int64_t>(a.nseq) * H;
     for (int64_t s = blockIdx.x; s < S; s += gridDim.x) {
         const int b = static_cast<int>(s / H), h = static_cast<int>(s % H);
         if (b >= us.b_lo && b < us.b_hi) {   // the thread whose run holds sequence b
             int64_t p = us.start;
-            for (int bb = us.b_lo; bb < b; ++bb) p += static_cast<int64_t>(H) * seq_work<G>(a, bb).u;
-            const int64_t u = seq_work<G>(a, b).u;
+            for (int bb = us.b_lo; bb < b; ++bb) p += static_cast<int64_t>(H) * seq_work<G, MQ>(a, bb).u;
+            const int64_t u = seq_work<G, MQ>(a, b).u;
             stream_at[0] = p + h * u;
             stream_at[1] = u;
         }
@@ -1623,10 +1819,15 @@ __global__ void __launch_bounds__(kThreads) decode_merge_kernel(DecodeArgs a, in
         const int64_t Ps = stream_at[0], u = stream_at[1];
         __syncthreads();   // every thread has read stream_at
         if (u == 0) continue;
-        const StreamSegs ss = stream_segs(s, Ps, seq_work<G>(a, b), us.U, Ceff, stream_overhead(a));
+        const StreamSegs ss = stream_segs(s, Ps, seq_work<G, MQ>(a, b), us.U, Ceff, stream_overhead(a));
         if (ss.nseg < 2) continue;
         asm volatile("griddepcontrol.wait;" ::: "memory");   // returns at once after the first time
-        merge_stream<GQ>(a, ss, a.out + stream_row<GQ, MQ>(a, b, h) * kD);
+        const int64_t row = stream_row<GQ, MQ>(a, b, h);
+        if constexpr (MQ == kExtended)
+            merge_stream<GQ>(a, ss, a.out + row * kD, stream_heads<GQ, MQ>(a, h),
+                             a.lse == nullptr ? nullptr : a.lse + row);
+        else
+            merge_stream<GQ>(a, ss, a.out + row * kD);
     }
 }
 
@@ -1639,7 +1840,7 @@ cudaError_t launch_mma(const DecodeArgs& a, cudaStream_t stream) {
     decode_mma_kernel<KB, VB, DT, GQ, G, MQ><<<n, kThreads, smem, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int64_t S = static_cast<int64_t>(a.nseq) * a.H * (MQ ? a.n_query : 1);
+    const int64_t S = static_cast<int64_t>(a.nseq) * a.H * (MQ == kExtended ? a.n_part : MQ ? a.n_query : 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(S < kMergeCtas ? S : kMergeCtas));
     cfg.blockDim = dim3(kThreads);
@@ -1683,6 +1884,27 @@ cudaError_t launch_kv(const DecodeArgs& a, cudaStream_t stream) {
                                    : launch_gq<KB, VB, KIVI_BF16, 64>(a, stream);
     }
     return a.dtype == KIVI_F16 ? launch_gq<KB, VB, KIVI_F16, 32>(a, stream) : launch_gq<KB, VB, KIVI_BF16, 32>(a, stream);
+}
+
+// The extended modes (a window with sinks, weights per group): streams of ext_heads(g) heads.
+template <int KB, int VB, int DT, int G>
+cudaError_t launch_ext_gq(const DecodeArgs& a, cudaStream_t stream) {
+    switch (ext_heads(a.Hq / a.H)) {
+        case 1: return launch_mma<KB, VB, DT, 1, G, kExtended>(a, stream);
+        case 2: return launch_mma<KB, VB, DT, 2, G, kExtended>(a, stream);
+        case 4: return launch_mma<KB, VB, DT, 4, G, kExtended>(a, stream);
+        default: return launch_mma<KB, VB, DT, 8, G, kExtended>(a, stream);
+    }
+}
+
+template <int KB, int VB>
+cudaError_t launch_ext_kv(const DecodeArgs& a, cudaStream_t stream) {
+    if (a.G == 64) {
+        return a.dtype == KIVI_F16 ? launch_ext_gq<KB, VB, KIVI_F16, 64>(a, stream)
+                                   : launch_ext_gq<KB, VB, KIVI_BF16, 64>(a, stream);
+    }
+    return a.dtype == KIVI_F16 ? launch_ext_gq<KB, VB, KIVI_F16, 32>(a, stream)
+                               : launch_ext_gq<KB, VB, KIVI_BF16, 32>(a, stream);
 }
 
 }  // namespace

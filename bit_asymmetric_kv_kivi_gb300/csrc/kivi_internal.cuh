@@ -170,7 +170,18 @@ struct DecodeArgs {
     int32_t* counters;              // [nseq][H] split tickets (workspace)
     float* partials;                // [nseq][Hq][max_splits][D + 4] (workspace)
     int32_t* status;
+    // extended modes only (a window with sinks, weights per group, any query group)
+    int window = 0, sinks = 0;      // window 0: every token is visible
+    int n_part = 0;                 // streams of ext_heads(Hq / H) heads per kv head
+    int max_tiles = 0;              // tiles of 32 tokens per sequence in stats
+    float2* stats = nullptr;        // [nseq][max_tiles][Hq] (running max, sum of exponentials), or null
+    float* lse = nullptr;           // [nseq][Hq] log2 of the sum of exponentials, or null
 };
+
+// Query heads of one stream of the extended modes: the smallest of 1, 2, 4 and 8 that holds the
+// query group, or 8 with several streams per kv head beyond that.
+constexpr int ext_heads(int g) { return g <= 1 ? 1 : g == 2 ? 2 : g <= 4 ? 4 : 8; }
+constexpr int ext_parts(int g) { return (g + ext_heads(g) - 1) / ext_heads(g); }
 
 // Bound on the persistent decode grid (CTAs); sizes its workspace.
 constexpr int kDecodeMaxCtas = 1024;
@@ -198,5 +209,39 @@ cudaError_t launch_decode_k2v2(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_k2v4(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_k4v2(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_k4v4(const DecodeArgs& a, cudaStream_t stream);
+// The extended modes of the same kernels.
+cudaError_t launch_ext_k2v2(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_ext_k2v4(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_ext_k4v2(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_ext_k4v4(const DecodeArgs& a, cudaStream_t stream);
+cudaError_t launch_ext(const DecodeArgs& a, cudaStream_t stream);
+
+// Per-group attention weights from the tile statistics of an extended decode (a.stats, a.lse).
+struct GroupWeightArgs {
+    int G, R, Hq, nseq, max_kv_len, max_tiles, stride;
+    const kivi_seq* seqs;
+    const int32_t* kv_len;
+    const float2* stats;
+    const float* lse;
+    const float* in;                // [nseq][stride], or null
+    float* out;                     // [nseq][stride]
+    float decay;
+};
+cudaError_t launch_group_weights(const GroupWeightArgs& a, cudaStream_t stream);
+
+// Eviction of packed groups by weight.
+struct EvictArgs {
+    int kb, vb, G, D, R, H;
+    int nseq, stride, keep, sink, recent;
+    const kivi_seq* seqs;
+    int32_t* kv_len;
+    float* weights;                 // [nseq][stride]
+    int32_t* map;                   // scratch [nseq][stride]
+    int32_t* cut;                   // scratch [nseq][2]: groups dropped, first dropped group
+    int32_t* status;
+};
+// Longest ring (tokens) whose turn fits shared memory.
+constexpr int kMaxTurnRing = 12800;
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace kivi

@@ -306,6 +306,88 @@ kivi_status kivi_decode_attn_static(const kivi_cfg* cfg, int32_t nseq, const kiv
                                     float softmax_scale, int32_t max_kv_len, int32_t* status_dev,
                                     void* stream);
 
+/* ---------------------------------------------------------------- windows, weights, eviction */
+
+/*
+ * Decode attention over a sliding window with sinks: kivi_decode_attn for a query that
+ * sees only the newest `window` tokens and the first `sinks` ones,
+ *   token t of a sequence of kv_len_b tokens is visible iff t >= kv_len_b - window or t < sinks.
+ * Tiles without a visible token are not read. The pages that describe KIVI have no window;
+ * the cache keeps every token (kivi_evict_groups drops some). Positions are places in the
+ * cache: after an eviction the sinks are its first groups, and the window its newest tokens.
+ *   window     0 means no window (every token is visible; sinks is then ignored)
+ *   sinks      may be 0, may end inside a group and may overlap the window
+ *   the rest   as kivi_decode_attn, with kivi_decode_ext_workspace_bytes() for the size
+ * Any query group up to 32 (groups of 3 run as streams of 4 heads, 5 to 7 as streams of 8,
+ * larger ones as several streams of 8). Device errors, empty sequences, the domain of q
+ * and the workspace (zero-filled before its first use, zero again after every call, shared
+ * with kivi_decode_attn and kivi_decode_multi_attn) as kivi_decode_attn.
+ * Errors: KIVI_ERR_ARG for a negative window or sinks.
+ */
+kivi_status kivi_decode_window_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev,
+                                    const int32_t* kv_len_dev, const void* q_dev, float* out_dev,
+                                    float softmax_scale, int32_t window, int32_t sinks, int32_t max_kv_len,
+                                    void* workspace_dev, size_t workspace_bytes, int32_t* status_dev,
+                                    void* stream);
+
+/* Workspace bytes of kivi_decode_window_attn and kivi_decode_attn_weights; 0 on a bad config. */
+size_t kivi_decode_ext_workspace_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_kv_len);
+
+/*
+ * Decode attention that also collects the attention weight of every G-token group, in the
+ * same pass over the cache (what kivi_evict_groups chooses by). With p the softmax weights of
+ * kivi_decode_attn and group j the tokens [j G, (j + 1) G), packed or not:
+ *   out            as kivi_decode_attn
+ *   weights_out[b][j] = decay * weights_in[b][j] + sum over query heads and tokens of group j of p
+ *                    for j < ceil(kv_len_b / G), and 0 for the groups behind them
+ *   weights_in_dev, weights_out_dev  [nseq][weights_stride] fp32; they may be the same array;
+ *                  weights_in_dev may be NULL (taken as 0), and is not read where decay is 0
+ *   weights_stride groups per row, weights_stride * G >= max_kv_len
+ *   decay          1 sums over the steps, less lets old steps fade, 0 keeps this step only
+ *   scratch_dev, scratch_bytes  at least kivi_decode_weights_scratch_bytes(), of any contents;
+ *                  calls that share it must not overlap
+ *   the rest       as kivi_decode_window_attn without a window
+ * A sequence with a device error (KIVI_ERR_LENGTH) gets NaN output and weights_out = weights_in
+ * (0 where that is NULL). Sums are fp32 in a fixed order.
+ * Errors: KIVI_ERR_ARG for a stride too small or a decay that is not finite.
+ */
+kivi_status kivi_decode_attn_weights(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev,
+                                     const int32_t* kv_len_dev, const void* q_dev, float* out_dev,
+                                     const float* weights_in_dev, float* weights_out_dev, int32_t weights_stride,
+                                     float decay, float softmax_scale, int32_t max_kv_len, void* workspace_dev,
+                                     size_t workspace_bytes, void* scratch_dev, size_t scratch_bytes,
+                                     int32_t* status_dev, void* stream);
+size_t kivi_decode_weights_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_kv_len);
+
+/*
+ * Eviction by accumulated weight: every sequence with more than keep_groups packed groups is
+ * cut to keep_groups of them. The first sink_groups and the last recent_groups packed groups
+ * stay; of the others those of largest weight (equal weights: the lower index; NaN
+ * counts as the smallest). Kept groups keep their order. A group is the unit because keys
+ * are quantized over its G tokens; the residual window always stays. The pages that describe
+ * KIVI do not drop tokens.
+ *   seqs_dev     contiguous sequences: the packed buffers are closed up in place. Paged ones: the
+ *                block table is permuted in place (it has to be writable): the kept groups' pages
+ *                first, then the dropped groups' pages, which the next groups to be packed
+ *                will overwrite; entries from the old packed count on are untouched.
+ *   kv_len_dev   in/out: less m G for a sequence that lost m groups; its residual rings are turned
+ *                by m G slots (slots follow positions), whole rows of unspecified contents included
+ *   weights_dev  [nseq][weights_stride] fp32, in/out: closed up the same way, the weights of groups that
+ *                are not packed yet behind those of the kept ones, zeros behind them
+ *   scratch_dev, scratch_bytes  at least kivi_evict_scratch_bytes(), of any contents; calls that share it
+ *                must not overlap
+ *   status_dev   one int32
+ * Any head_dim of the codec. Device error KIVI_ERR_LENGTH: kv_len_b negative, more tokens than the sequence
+ * can hold or more than weights_stride groups; that sequence is left unchanged.
+ * Errors: KIVI_ERR_ARG for a negative count or sink_groups + recent_groups > keep_groups;
+ * KIVI_ERR_UNSUPPORTED for R + G > 12800; KIVI_ERR_WORKSPACE for the scratch.
+ */
+kivi_status kivi_evict_groups(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev, int32_t* kv_len_dev,
+                              float* weights_dev, int32_t weights_stride, int32_t keep_groups, int32_t sink_groups,
+                              int32_t recent_groups, void* scratch_dev, size_t scratch_bytes, int32_t* status_dev,
+                              void* stream);
+size_t kivi_evict_scratch_bytes(int32_t nseq, int32_t weights_stride);
+
 /* ---------------------------------------------------------------- sizes and helpers */
 
 /*
