@@ -85,6 +85,11 @@ def lib() -> ctypes.CDLL:
             L.kivi_decode_attn_weights.restype = I32
             L.kivi_decode_weights_scratch_bytes.argtypes = [CFG, I32, I32]
             L.kivi_decode_weights_scratch_bytes.restype = ctypes.c_size_t
+            L.kivi_chunk_attn.argtypes = [CFG, I32, P, P, P, P, P, I32, P, P, P, ctypes.c_float, I32, I32, I32, P,
+                                          ctypes.c_size_t, P, P]
+            L.kivi_chunk_attn.restype = I32
+            L.kivi_chunk_scratch_bytes.argtypes = [CFG, I32, I32]
+            L.kivi_chunk_scratch_bytes.restype = ctypes.c_size_t
             L.kivi_evict_groups.argtypes = [CFG, I32, P, P, P, I32, I32, I32, I32, P, ctypes.c_size_t, P, P]
             L.kivi_evict_groups.restype = I32
             L.kivi_evict_scratch_bytes.argtypes = [I32, I32]
@@ -489,6 +494,54 @@ class KVCache:
                                                   scale, mkl, _ptr(ws), ws.numel(), _ptr(sc), sc.numel(),
                                                   _ptr(self.status), _stream(q.device)), "kivi_decode_attn_weights")
         return out, weights_out
+
+    def chunk_attn(self, q: torch.Tensor, q_start: torch.Tensor, k_ptrs: torch.Tensor, v_ptrs: torch.Tensor,
+                   n_new: torch.Tensor, max_new: int, out: torch.Tensor | None = None, window: int = 0, sinks: int = 0,
+                   softmax_scale: float | None = None, max_kv_len: int | None = None) -> torch.Tensor:
+        """Attention of a chunk of new tokens per sequence to the cache and, causally, to the chunk itself,
+        before it is appended (kivi_chunk_attn). q [rows][Hq][D] (cfg dtype), sequence b's queries from row
+        q_start[b] (int32) on; k_ptrs, v_ptrs, n_new, max_new as append_ptrs. Returns out like q."""
+        cfg = self.cfg
+        if q.dim() != 3:
+            raise ValueError("q must be [rows][Hq][D]")
+        _require(q, "q", (q.shape[0], cfg.num_q_heads, cfg.head_dim), cfg.torch_dtype, self.device)
+        for name, t, dt in (("q_start", q_start, torch.int32), ("k_ptrs", k_ptrs, torch.int64),
+                            ("v_ptrs", v_ptrs, torch.int64), ("n_new", n_new, torch.int32)):
+            _require(t, name, (self.nseq,), dt, q.device)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _require(out, "out", q.shape, cfg.torch_dtype, q.device)
+        scale = 1.0 / cfg.head_dim ** 0.5 if softmax_scale is None else softmax_scale
+        mkl = int(self.max_len if max_kv_len is None else max_kv_len)
+        with torch.cuda.device(q.device):
+            sc = self._any(int(lib().kivi_chunk_scratch_bytes(cfg.c(), self.nseq, int(max_new))))
+            _check(lib().kivi_chunk_attn(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(k_ptrs),
+                                         _ptr(v_ptrs), _ptr(n_new), int(max_new), _ptr(q), _ptr(q_start), _ptr(out),
+                                         float(scale), int(window), int(sinks), mkl, _ptr(sc), sc.numel(),
+                                         _ptr(self.status), _stream(q.device)), "kivi_chunk_attn")
+        return out
+
+    def chunk(self, q, k_new, v_new, window: int = 0, sinks: int = 0, softmax_scale: float | None = None):
+        """chunk_attn on lists: per sequence q [n_b][Hq][D], k_new and v_new [Hkv][n_b][D] -> a list of
+        outputs like q. (Tables of pointers are made and copied per call; chunk_attn takes them as given.)"""
+        q, k_new, v_new = list(q), list(k_new), list(v_new)
+        cfg = self.cfg
+        if not len(q) == len(k_new) == len(v_new) == self.nseq:
+            raise ValueError("one q, k_new and v_new for each sequence")
+        n = [int(x.shape[0]) for x in q]
+        for m, k, v in zip(n, k_new, v_new):
+            for t in (k, v):
+                if m:
+                    _require(t, "k_new and v_new", (cfg.num_kv_heads, m, cfg.head_dim), cfg.torch_dtype, self.device)
+        dev = self.kv_len.device
+        start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+        kp = torch.tensor([k.data_ptr() if m else 0 for m, k in zip(n, k_new)], dtype=torch.int64).to(dev)
+        vp = torch.tensor([v.data_ptr() if m else 0 for m, v in zip(n, v_new)], dtype=torch.int64).to(dev)
+        out = self.chunk_attn(torch.cat(q), torch.from_numpy(start[:-1].copy()).to(dev), kp, vp,
+                              torch.tensor(n, dtype=torch.int32).to(dev), max(n, default=0), window=window, sinks=sinks,
+                              softmax_scale=softmax_scale)
+        return list(out.split(n))
 
     def evict(self, weights: torch.Tensor, keep_groups: int, sink_groups: int = 0, recent_groups: int = 0) -> None:
         """Cut every sequence to its keep_groups packed groups of largest weight (the first

@@ -322,6 +322,61 @@ kivi_status kivi_decode_attn_weights(const kivi_cfg* cfg, int32_t nseq, const ki
     return from_cuda(kivi::launch_group_weights(w, s));
 }
 
+size_t kivi_chunk_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_new) {
+    if (!cfg_ok(cfg) || nseq < 0 || max_new < 0) return 0;
+    int pairs, tiles;
+    size_t rec;
+    kivi::chunk_plan(cfg->num_q_heads, cfg->num_kv_heads, max_new, &pairs, &tiles, &rec);
+    return rec + kivi::kChunkMaxCtas * sizeof(kivi::ChunkInfo);
+}
+
+kivi_status kivi_chunk_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev, const int32_t* kv_len_dev,
+                            const void* const* k_new_dev, const void* const* v_new_dev, const int32_t* n_new_dev,
+                            int32_t max_new, const void* q_dev, const int32_t* q_start_dev, void* out_dev,
+                            float softmax_scale, int32_t window, int32_t sinks, int32_t max_kv_len,
+                            void* scratch_dev, size_t scratch_bytes, int32_t* status_dev, void* stream) {
+    if (!cfg_ok(cfg)) return KIVI_ERR_ARG;
+    if (nseq < 0 || nseq > 65535 || max_new < 0 || max_kv_len < 0 || window < 0 || sinks < 0 || !isfinite(softmax_scale))
+        return KIVI_ERR_ARG;
+    const int64_t g = cfg->num_q_heads / cfg->num_kv_heads;
+    if (cfg->head_dim != 128 || g * max_new > INT32_MAX - 256 || static_cast<int64_t>(max_kv_len) + max_new > INT32_MAX - 256)
+        return KIVI_ERR_UNSUPPORTED;
+    if (nseq == 0 || max_new == 0) return KIVI_OK;
+    if (seqs_dev == nullptr || kv_len_dev == nullptr || k_new_dev == nullptr || v_new_dev == nullptr ||
+        n_new_dev == nullptr || q_dev == nullptr || q_start_dev == nullptr || out_dev == nullptr)
+        return KIVI_ERR_ARG;
+    if (scratch_dev == nullptr || scratch_bytes < kivi_chunk_scratch_bytes(cfg, nseq, max_new)) return KIVI_ERR_WORKSPACE;
+    kivi::ChunkArgs a;
+    size_t rec;
+    kivi::chunk_plan(cfg->num_q_heads, cfg->num_kv_heads, max_new, &a.pairs, &a.rec_tiles, &rec);
+    a.kb = cfg->k_bits;
+    a.vb = cfg->v_bits;
+    a.G = cfg->group;
+    a.R = cfg->residual;
+    a.Hq = cfg->num_q_heads;
+    a.H = cfg->num_kv_heads;
+    a.dtype = cfg->dtype;
+    a.nseq = nseq;
+    a.max_new = max_new;
+    a.max_kv_len = max_kv_len;
+    a.window = window;
+    a.sinks = sinks;
+    a.ctas = 0;
+    a.seqs = seqs_dev;
+    a.kv_len = kv_len_dev;
+    a.k_new = k_new_dev;
+    a.v_new = v_new_dev;
+    a.n_new = n_new_dev;
+    a.q_start = q_start_dev;
+    a.q = q_dev;
+    a.out = out_dev;
+    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.records = static_cast<float*>(scratch_dev);
+    a.info = reinterpret_cast<kivi::ChunkInfo*>(static_cast<char*>(scratch_dev) + rec);
+    a.status = status_dev;
+    return from_cuda(kivi::launch_chunk(a, static_cast<cudaStream_t>(stream)));
+}
+
 size_t kivi_evict_scratch_bytes(int32_t nseq, int32_t weights_stride) {
     if (nseq < 0 || weights_stride < 0) return 0;
     return static_cast<size_t>(nseq) * (static_cast<size_t>(weights_stride) + 2) * sizeof(int32_t);

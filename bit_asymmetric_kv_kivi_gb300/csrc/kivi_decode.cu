@@ -59,6 +59,21 @@ cudaError_t launch_ext(const DecodeArgs& a, cudaStream_t stream) {
     return a.vb == 2 ? launch_ext_k4v2(a, stream) : launch_ext_k4v4(a, stream);
 }
 
+// Chunk attention: rows are (query, head) pairs of a kv head in tiles of 128, two tiles to a
+// CTA; records of 128 x (128 + 2) floats, two per CTA and row tile.
+void chunk_plan(int Hq, int H, int max_new, int* pairs, int* rec_tiles, size_t* rec_bytes) {
+    const int64_t rows = static_cast<int64_t>(max_new) * (Hq / H);
+    *pairs = static_cast<int>((rows + 255) / 256);
+    *rec_tiles = rows > 128 ? 2 : 1;
+    *rec_bytes = static_cast<size_t>(kChunkMaxCtas) * 2 * *rec_tiles * 128 * (128 + 2) * sizeof(float);
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream) {
+    if (a.nseq == 0 || a.max_new == 0) return cudaSuccess;
+    if (a.kb == 2) return a.vb == 2 ? launch_chunk_k2v2(a, stream) : launch_chunk_k2v4(a, stream);
+    return a.vb == 2 ? launch_chunk_k4v2(a, stream) : launch_chunk_k4v4(a, stream);
+}
+
 // Multi-query attention: packed splits of a whole number of 32-token tiles, about an eighth
 // of the longest sequence in 256-token steps between 1024 and 4096 tokens, plus one split
 // for the residual window; one record of kD + 4 floats per (split, virtual head), the

@@ -216,6 +216,39 @@ cudaError_t launch_ext_k4v2(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_ext_k4v4(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_ext(const DecodeArgs& a, cudaStream_t stream);
 
+// Attention of a chunk of new tokens (kivi_chunk_attn).
+struct ChunkInfo {
+    int32_t b, row0, rows, h, nseg;   // a row tile pair that a CTA began and others went on with (nseg CTAs in all)
+};
+struct ChunkArgs {
+    int kb, vb, G, R, Hq, H, dtype;
+    int nseq, max_new, max_kv_len;
+    int window, sinks;              // window 0: no window
+    int pairs;                      // pairs of row tiles of the longest chunk
+    int rec_tiles;                  // row tiles per record: 1 when no chunk has more than one
+    int ctas;                       // set by the launch
+    const kivi_seq* seqs;
+    const int32_t* kv_len;
+    const void* const* k_new;
+    const void* const* v_new;
+    const int32_t* n_new;
+    const int32_t* q_start;
+    const void* q;
+    void* out;
+    float scale_log2;
+    float* records;                 // scratch
+    ChunkInfo* info;                // scratch, one per CTA
+    int32_t* status;
+};
+constexpr int kChunkMaxCtas = 160;  // one per SM of a GB300, rounded up; sizes the scratch
+cudaError_t launch_chunk_k2v2(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk_k2v4(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk_k4v2(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk_k4v4(const ChunkArgs& a, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t stream);
+// Bytes of the records (info behind them), and the row tile counts of a call.
+void chunk_plan(int Hq, int H, int max_new, int* pairs, int* rec_tiles, size_t* rec_bytes);
+
 // Per-group attention weights from the tile statistics of an extended decode (a.stats, a.lse).
 struct GroupWeightArgs {
     int G, R, Hq, nseq, max_kv_len, max_tiles, stride;

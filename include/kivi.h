@@ -360,6 +360,40 @@ kivi_status kivi_decode_attn_weights(const kivi_cfg* cfg, int32_t nseq, const ki
 size_t kivi_decode_weights_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_kv_len);
 
 /*
+ * Attention of a chunk of new tokens, before they are appended: chunked prefill, continuous
+ * batching (chunks of any lengths side by side, single tokens among them), or the check of
+ * draft tokens that may yet be dropped. Query i of sequence b stands at position kv_len_b + i:
+ *   out[i][hq][:] = sum over visible t of softmax_t(softmax_scale * q[i][hq] . k_t) v_t
+ * t < kv_len_b: the cache (packed tokens dequantized as c*s + z, residual tokens as stored);
+ * kv_len_b <= t <= kv_len_b + i: the chunk itself, in full precision, causally. With a window, t is visible
+ * iff t > kv_len_b + i - window or t < sinks. ("KIVI: A Tuning-Free Asymmetric 2bit Quantization for KV Cache"
+ * quantizes the cache and leaves the tokens of a prefill pass as they are while it runs; the
+ * pages show no chunked pass.) The cache is not changed; kivi_append_flush with the same
+ * k_new, v_new and n_new appends the chunk afterwards.
+ *   k_new_dev, v_new_dev, n_new_dev, max_new   as kivi_append_flush: [Hkv][n_new_b][D] dtype per sequence
+ *   q_dev       rows [Hq][D] dtype; sequence b's queries are rows q_start_b ... q_start_b + n_new_b - 1
+ *   q_start_dev [nseq] int32 (need not be ascending; rows of different sequences do not overlap)
+ *   out_dev     rows as q_dev, [Hq][D] dtype, rounded once from fp32; rows of no sequence are not written
+ *   window      0 means no window (sinks is then ignored)
+ *   max_kv_len  host bound on every kv_len_b (checked on the device; it does not size the grid)
+ *   scratch_dev, scratch_bytes  at least kivi_chunk_scratch_bytes(), of any contents; calls that share it
+ *               must not overlap
+ *   status_dev  one int32 (may be NULL)
+ * The products run on the tensor cores in f16 with fp32 accumulation: dequantized tokens and
+ * probabilities are rounded to f16 (2^-11 relative). Domain: finite q with |softmax_scale * q| <= 2^100; finite k_new,
+ * v_new with magnitudes up to 65504 (the codec's domain), also in rows that no query sees.
+ * Device error KIVI_ERR_LENGTH: n_new_b outside [0, max_new] (nothing is written for b), or kv_len_b outside [0,
+ * max_kv_len] or more tokens than the sequence can hold (its output rows are NaN).
+ * Errors: KIVI_ERR_ARG for a negative window, sinks or size; KIVI_ERR_UNSUPPORTED unless D == 128.
+ */
+kivi_status kivi_chunk_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev, const int32_t* kv_len_dev,
+                            const void* const* k_new_dev, const void* const* v_new_dev, const int32_t* n_new_dev,
+                            int32_t max_new, const void* q_dev, const int32_t* q_start_dev, void* out_dev,
+                            float softmax_scale, int32_t window, int32_t sinks, int32_t max_kv_len,
+                            void* scratch_dev, size_t scratch_bytes, int32_t* status_dev, void* stream);
+size_t kivi_chunk_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_new);
+
+/*
  * Eviction by accumulated weight: every sequence with more than keep_groups packed groups is
  * cut to keep_groups of them. The first sink_groups and the last recent_groups packed groups
  * stay; of the others those of largest weight (equal weights: the lower index; NaN

@@ -1,0 +1,189 @@
+"""GPU tests of chunk attention (kivi_chunk_attn): chunks of any lengths over the packed cache against
+a 64-bit statement, the cache untouched, and the chunk appended afterwards."""
+import numpy as np
+import pytest
+import torch
+
+import bit_asymmetric_kv_kivi_gb300 as kivi
+import oracle
+import synth
+from gpu_util import TORCH_DT, dev_tensor, host_bits
+from ops_ref import attend, chunk_bounds, dense, visible, widen
+from test_gpu_window import build
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def chunk_inputs(wl, new, seed=0):
+    """Per sequence: queries [n][Hq][D] and the next n keys and values [H][n][D] (bit patterns)."""
+    rng = np.random.default_rng(seed)
+    q = [synth.to_dtype_bits(rng.standard_normal((n, wl.num_q_heads, 128)), wl.dtype) for n in new]
+    kv = [wl.kv_seq(b, wl.lengths[b], n) for b, n in enumerate(new)]
+    return q, [x for x, _ in kv], [x for _, x in kv]
+
+
+def check(wl, refs, q, k, v, outs, window, sinks):
+    dt = refs[0].cfg.dtype
+    num = den = lim = 0.0
+    for b, r in enumerate(refs):
+        n = q[b].shape[0]
+        if n == 0:
+            continue
+        qf = widen(q[b], dt)
+        kc, vc, _, _ = dense(r)
+        kk, vv = np.concatenate([kc, widen(k[b], dt)], 1), np.concatenate([vc, widen(v[b], dt)], 1)
+        want, p = attend(qf, kk, vv, visible(r.L + n, n, window, sinks), wl.softmax_scale)
+        got = outs[b].double().cpu().numpy()
+        el, rel = chunk_bounds(qf, kk, vv, p, want, wl.softmax_scale, HALF[wl.dtype])
+        bad = ~(np.abs(got - want) <= el)
+        assert not bad.any(), (b, r.L, n, np.argwhere(bad)[:4], np.abs(got - want).max(), el.max())
+        num, den, lim = num + ((got - want) ** 2).sum(), den + (want ** 2).sum(), max(lim, rel)
+    assert den == 0 or np.sqrt(num / den) <= lim, (np.sqrt(num / den), lim)
+
+
+def run(cache, wl, q, k, v, window=0, sinks=0):
+    d = lambda xs: [dev_tensor(x, wl.dtype) for x in xs]   # noqa: E731
+    outs = cache.chunk(d(q), d(k), d(v), window=window, sinks=sinks, softmax_scale=wl.softmax_scale)
+    torch.cuda.synchronize()
+    assert int(cache.status.item()) == 0
+    return outs
+
+
+@pytest.mark.parametrize("n", [1, 2, 5, 40, 127, 128, 300])
+@pytest.mark.parametrize("L", [0, 1, 100, 160, 161, 1000])
+def test_one_sequence(n, L):
+    wl = synth.Workload("one", 1, 1, 1, 128, (L,), "f16", seed=L + n)
+    cache, refs = build(wl, 2, 2, 32, 128, 1024)
+    q, k, v = chunk_inputs(wl, [n], n)
+    check(wl, refs, q, k, v, run(cache, wl, q, k, v), 0, 0)
+
+
+@pytest.mark.parametrize("g", [1, 3, 4, 7, 8, 40])
+@pytest.mark.parametrize("kb,vb,G,R,dtype,paged", [(2, 2, 32, 128, "bf16", True), (4, 4, 64, 64, "f16", False),
+                                                   (2, 4, 32, 32, "f16", True), (4, 2, 64, 128, "bf16", False)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (130, 4), (300, 200), (5000, 4)])
+def test_ragged_batch(g, kb, vb, G, R, dtype, paged, window, sinks):
+    """Empty and one-token chunks next to long ones, empty caches and every edge of the packed split."""
+    lengths, new = (0, 700, 33, 161, 0, 1500, 95), (130, 1, 0, 7, 1, 65, 260)
+    H = 2
+    wl = synth.Workload("ragged", len(lengths), g * H, H, 128, lengths, dtype, seed=70 + g)
+    cache, refs = build(wl, kb, vb, G, R, 1536, paged=paged)
+    q, k, v = chunk_inputs(wl, new, g)
+    check(wl, refs, q, k, v, run(cache, wl, q, k, v, window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("H,g,n", [(1, 4, 3), (2, 1, 1), (1, 8, 64)])
+def test_long_cache_split_over_ctas(H, g, n):
+    """Few rows over a long cache: every CTA takes a part and the parts are joined."""
+    wl = synth.Workload("split", 1, H * g, H, 128, (20000,), "f16", seed=5)
+    cache, refs = build(wl, 2, 2, 32, 128, 20000)
+    q, k, v = chunk_inputs(wl, [n])
+    for window, sinks in ((0, 0), (9000, 5)):
+        check(wl, refs, q, k, v, run(cache, wl, q, k, v, window, sinks), window, sinks)
+
+
+def test_large_scores_and_scales():
+    """Scores that leave one token all the weight, queries far from 1, and negative and zero scales."""
+    wl = synth.Workload("scores", 2, 4, 1, 128, (300, 20), "bf16", seed=3)
+    cache, refs = build(wl, 2, 2, 32, 128, 512)
+    q, k, v = chunk_inputs(wl, (150, 9))
+    f = [widen(x, oracle.BF16) for x in q]
+    for s in (2.0 ** 12, 2.0 ** -30):
+        qs = [synth.to_dtype_bits(x * s, "bf16") for x in f]
+        w = wl
+        for scale in (w.softmax_scale / s, -w.softmax_scale / s, 0.0, 3 * w.softmax_scale / s):
+            d = lambda xs: [dev_tensor(x, "bf16") for x in xs]   # noqa: E731
+            outs = cache.chunk(d(qs), d(k), d(v), softmax_scale=scale)
+            for b, r in enumerate(refs):
+                qf = widen(qs[b], oracle.BF16)
+                kc, vc, _, _ = dense(r)
+                kk, vv = (np.concatenate([c, widen(x[b], oracle.BF16)], 1) for c, x in ((kc, k), (vc, v)))
+                n = qf.shape[0]
+                want, p = attend(qf, kk, vv, visible(r.L + n, n, 0, 0), scale)
+                el, _ = chunk_bounds(qf, kk, vv, p, want, abs(scale), HALF["bf16"])
+                assert (np.abs(outs[b].double().cpu().numpy() - want) <= el).all()
+
+
+def test_rows_between_sequences_and_bad_lengths():
+    """Rows that no sequence owns stay as they were; a bad count writes nothing, a bad length NaN."""
+    lengths, new = (300, 50, 200), (5, 3, 4)
+    wl = synth.Workload("rows", 3, 8, 2, 128, lengths, "f16", seed=12)
+    cache, refs = build(wl, 2, 2, 32, 128, 512)
+    q, k, v = chunk_inputs(wl, new)
+    start = [20, 2, 10]
+    qd = torch.zeros((30, 8, 128), dtype=torch.float16, device="cuda")
+    for b in range(3):
+        qd[start[b]:start[b] + new[b]] = dev_tensor(q[b], "f16")
+    out = torch.full_like(qd, 7.0)
+    kd, vd = [dev_tensor(x, "f16") for x in k], [dev_tensor(x, "f16") for x in v]
+    i = lambda x, t: torch.tensor(x, dtype=t, device="cuda")   # noqa: E731
+    args = (qd, i(start, torch.int32), i([x.data_ptr() for x in kd], torch.int64), i([x.data_ptr() for x in vd], torch.int64))
+    cache.chunk_attn(*args, i(new, torch.int32), 5, out=out, softmax_scale=wl.softmax_scale)
+    assert int(cache.status.item()) == 0
+    check(wl, refs, q, k, v, [out[s:s + n] for s, n in zip(start, new)], 0, 0)
+    owned = torch.zeros(30, dtype=torch.bool)
+    for s, n in zip(start, new):
+        owned[s:s + n] = True
+    assert bool((out[~owned.cuda()] == 7).all())
+    out.fill_(7.0)
+    cache.chunk_attn(*args, i((5, 9, 4), torch.int32), 5, out=out, softmax_scale=wl.softmax_scale, max_kv_len=250)
+    assert int(cache.status.item()) == kivi.ERR_LENGTH
+    assert bool(out[20:25].isnan().all()) and bool((out[2:10] == 7).all())
+    check(wl, refs[2:], q[2:], k[2:], v[2:], [out[10:14]], 0, 0)
+
+
+def test_cache_untouched_then_appended_in_chunks():
+    """A prompt in chunks of odd sizes: attention, then append; the state equals the oracle's and every
+    chunk's attention the 64-bit statement on it. Captured calls read the lengths at replay."""
+    H, g = 2, 4
+    wl = synth.Workload("prefill", 2, g * H, H, 128, (0, 0), "bf16", seed=44)
+    cache, refs = build(wl, 2, 2, 32, 64, 1024, paged=True)
+    pos = [0, 0]
+    for step, n in enumerate(((200, 1), (1, 130), (77, 64), (300, 300))):
+        at = synth.Workload("prefill", 2, g * H, H, 128, tuple(pos), "bf16", seed=44)
+        q, k, v = chunk_inputs(at, n, step)
+        before = [cache.seq_numpy(b) for b in range(2)]
+        check(wl, refs, q, k, v, run(cache, wl, q, k, v), 0, 0)
+        for b in range(2):
+            after = cache.seq_numpy(b)
+            assert all(np.array_equal(before[b][x], after[x]) for x in after)
+            assert refs[b].append(k[b], v[b]) == oracle.OK
+            pos[b] += n[b]
+        cache.append([dev_tensor(x, "bf16") for x in k], [dev_tensor(x, "bf16") for x in v])
+    from gpu_util import assert_state_equal
+    for b in range(2):
+        assert_state_equal(cache, b, refs[b])
+
+
+def test_captured_and_on_another_stream():
+    wl = synth.Workload("cap", 2, 8, 2, 128, (500, 90), "f16", seed=21)
+    cache, refs = build(wl, 2, 2, 32, 128, 1024)
+    q, k, v = chunk_inputs(wl, (33, 20))
+    kd, vd = [dev_tensor(x, "f16") for x in k], [dev_tensor(x, "f16") for x in v]
+    i = lambda x, t: torch.tensor(x, dtype=t, device="cuda")   # noqa: E731
+    qd = torch.cat([dev_tensor(x, "f16") for x in q])
+    n = i((33, 20), torch.int32)
+    args = (qd, i((0, 33), torch.int32), i([x.data_ptr() for x in kd], torch.int64), i([x.data_ptr() for x in vd], torch.int64), n, 40)
+    out = torch.zeros_like(qd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cache.chunk_attn(*args, out=out, softmax_scale=wl.softmax_scale, max_kv_len=900)
+    torch.cuda.synchronize()
+    check(wl, refs, q, k, v, out.split((33, 20)), 0, 0)
+    first = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.chunk_attn(*args, out=out, softmax_scale=wl.softmax_scale, max_kv_len=900)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    n.copy_(i((1, 20), torch.int32))          # fewer tokens: same rows, read at replay
+    out.fill_(3.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((out[1:33] == 3).all()) and bool((out[:1] != 3).any())
