@@ -359,7 +359,7 @@ kivi_status kivi_chunk_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* s
     a.nseq = nseq;
     a.max_new = max_new;
     a.max_kv_len = max_kv_len;
-    a.window = window;
+    a.window = static_cast<int64_t>(window) >= static_cast<int64_t>(max_kv_len) + max_new ? 0 : window;   // hides nothing
     a.sinks = sinks;
     a.ctas = 0;
     a.seqs = seqs_dev;

@@ -30,17 +30,22 @@
 // tiles it sees plus an overhead; CTA c takes units [c U / C, (c + 1) U / C). A row tile that
 // several CTAs share leaves fp32 records (acc, max, sum) that chunk_merge_kernel joins.
 #pragma once
+#include <type_traits>
+
 #include "kivi_decode_impl.cuh"
 
 namespace kivi {
 namespace {
 
 constexpr int kChunkSoftmaxWarps = 8;
-constexpr int kChunkThreads = 17 * 32;
+constexpr int kChunkThreads = 20 * 32;
 constexpr int kRows = 128;                // rows of a row tile
 constexpr int kKeys = 128;                // tokens of a key tile
 constexpr int kOpBytes = kRows * kD * 2;  // one 128 x 128 f16 operand tile
 constexpr int kKvStages = 2;
+// Registers per thread of the softmax, operand and issue warpgroups: setmaxnreg moves them from
+// the launch's 96 x 640, and the three shares add up to it (256 x 152 + 256 x 72 + 128 x 32).
+constexpr int kSoftmaxRegs = 120, kOperandRegs = 88, kIssueRegs = 64;
 constexpr int kUnitOverhead = 3;          // units charged per (row tile pair, kv head)
 constexpr int kMinChunkUnits = 4;
 constexpr float kLag = 8.0f;              // log2 by which the softmax reference may lag behind
@@ -55,21 +60,23 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// How long one try may sleep: short tries made waiting warps take issue slots from working ones.
+constexpr uint32_t kSleepNs = 1000000;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSleepNs) : "memory");
     return ok != 0;
 }
 // Waits for a phase; gives up (and tells the other roles) after about two seconds, so that no
 // mistake in the schedule can hang the device.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-    if (mbar_try(bar, parity)) return true;
-    const long long t0 = clock64();
+    long long t0 = 0;
     while (!mbar_try(bar, parity)) {
-        if (*stop != 0) return false;
-        if (clock64() - t0 > 4000000000LL) {
+        const long long t = clock64();
+        if (t0 == 0) t0 = t;
+        if (*stop != 0 || t - t0 > 4000000000LL) {
             *stop = 1;
             return false;
         }
@@ -77,6 +84,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
+// One lane of the (converged) warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -98,6 +111,14 @@ __device__ __forceinline__ void tc_ld32(float (&r)[32], uint32_t addr) {
           "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tc_ld16(float (&r)[16], uint32_t addr) {
+    uint32_t* u = reinterpret_cast<uint32_t*>(r);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+          "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(addr));
+}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const float (&r)[32]) {
     const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
     asm volatile(
@@ -117,30 +138,45 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&u)[16]) 
         : "memory");
 }
 
+// Two fp32 at a time
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
+
 // Operand tiles in shared memory: two blocks of 64 channels, each 128 rows of 128 bytes with the
 // 16-byte chunks of a row XORed by its low three bits (the 128-byte swizzle).
 __device__ __forceinline__ uint32_t op_addr(int row, int chunk) {   // chunk of 8 channels, 0 .. 15
     return static_cast<uint32_t>((chunk >> 3) * (kRows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
-// Shared-memory descriptor, 128-byte swizzle. K-major (Q, K): rows of 8 every 1024 bytes. MN-major
-// (V: channels contiguous): 64-channel blocks every kRows * 128 bytes, groups of 8 tokens every 1024.
-__device__ __forceinline__ uint64_t op_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory descriptors, 128-byte swizzle, as (low word, high word): K-major (Q, K) has rows of 8
+// every 1024 bytes; MN-major (V: channels contiguous) has 64-channel blocks every kRows * 128 bytes
+// and groups of 8 tokens every 1024. Only the low word's address changes from one product to the next.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
 // f32 accumulator, f16 operands, N = M = 128; bit 16: B is MN-major
 constexpr uint32_t kIdescQK = (1u << 4) | ((kKeys / 8) << 17) | ((kRows / 16) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((kD / 8) << 17) | ((kRows / 16) << 24);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One K = 16 step, A from shared memory or from TMEM; acc 0 overwrites D, 1 adds to it.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)) : "memory");
+        "{ .reg .pred p; .reg .b64 x, y; mov.b64 x, {%1, %3}; mov.b64 y, {%2, %3}; setp.ne.b32 p, %5, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p; }"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(acc) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)) : "memory");
+        "{ .reg .pred p; .reg .b64 y; mov.b64 y, {%2, %3}; setp.ne.b32 p, %5, 0;"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p; }"
+        ::"r"(d), "r"(a), "r"(b), "r"(kDescHi), "r"(idesc), "r"(acc) : "memory");
 }
 
 // ---------------------------------------------------------------- the row of units
@@ -195,8 +231,8 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int64_t idx)
 }
 __device__ __forceinline__ int64_t item_units(const ChunkItem& it) { return it.nt > 0 ? it.nt + kUnitOverhead : 0; }
 
-// A CTA's share of the row of units. Every role walks it by itself: next() yields the segments
-// (a row tile pair of one kv head, listed key tiles [x0, x1)).
+// A CTA's share of the row of units; chunk_next yields its segments (a row tile pair of one kv
+// head, listed key tiles [x0, x1)).
 struct ChunkWalk {
     int64_t lo, hi, pos, idx;   // this CTA's units, first unit of item idx
     int64_t U;
@@ -232,16 +268,37 @@ __device__ __forceinline__ bool chunk_next(const ChunkArgs& a, ChunkWalk& w, Chu
     return false;
 }
 
+// Raw packed subtiles (32 tokens of one kv head) on their way from memory: codes, scales and
+// zeros of keys and values, as bulk copies. As many stages as fit beside the operand tiles.
+template <int KB, int VB>
+struct RawLayout {
+    static constexpr int kKc = 0, kKs = kTile * kD * KB / 8, kKz = kKs + kD * 2, kVc = kKz + kD * 2;
+    static constexpr int kVs = kVc + kTile * kD * VB / 8, kVz = kVs + 256, kBytes = kVz + 256;   // 128 of the last two used when G = 64
+    static constexpr int kStages = KB + VB == 4 ? 10 : KB + VB == 6 ? 8 : 6;
+};
+constexpr int kRawMax = 10;
+constexpr int kSegs = 4;                  // segments announced ahead (warp 18 walks, every role follows)
+constexpr int kSegReaders = 18;           // warps 0 .. 17
+
 struct ChunkShared {
     uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    uint64_t raw_full[kRawMax], raw_empty[kRawMax], hand_full, hand_empty, seg_full[kSegs], seg_empty[kSegs];
+    ChunkSeg seg[kSegs];
+    float hand_m[kRows], hand_l[kRows];   // state of the second softmax warpgroup at the end of a narrow segment
     int64_t warp_sum[kChunkThreads / 32];
     int64_t lo, hi, pos, idx, U;
     int C, h;
     uint32_t tmem;
     int stop;
 };
-constexpr int kChunkSmem = 2 * kOpBytes + 2 * kKvStages * kOpBytes + 1024 + static_cast<int>(sizeof(ChunkShared));
+template <int KB, int VB>
+constexpr int chunk_smem() {
+    constexpr int bytes = 2 * kOpBytes + 2 * kKvStages * kOpBytes + RawLayout<KB, VB>::kStages * RawLayout<KB, VB>::kBytes +
+                          1024 + static_cast<int>(sizeof(ChunkShared));
+    static_assert(bytes <= 227 * 1024, "shared memory of one CTA");
+    return bytes;
+}
 
 // ---------------------------------------------------------------- operand tiles
 
@@ -300,77 +357,87 @@ __device__ __forceinline__ void load8(uint32_t (&w)[8], const void* p) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// Where a sequence's tokens of one kv head lie.
-struct ChunkSrc {
-    const kivi_seq* sq;
-    const uint16_t *res, *fresh;   // this head's ring and new tokens (keys or values)
-    int64_t L, np, end;            // cached, packed, cached and new tokens
-    int ring;
-};
+__device__ __forceinline__ void store_rows(unsigned char* dst, int row, int span, const uint32_t (&o)[8]) {
+    *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+}
 
-// One thread's part of a key (VALUES false) or value tile: rows lo8 + 8 rh + 16 k of each 32-token
-// subtile, one 16-channel span, so that the eight lanes of a store phase hit eight rows
-// (distinct banks under the swizzle).
-template <int BITS, int DT, bool VALUES>
-__device__ __forceinline__ void fill_tile(const ChunkArgs& a, const ChunkSrc& s, int h, int64_t t0, unsigned char* dst,
-                                          int p) {
-    const int row_lo = (p & 7) + 8 * (p >> 6), span = (p >> 3) & 7;
+// A warp's part of a packed subtile (32 tokens): lane (row_lo = lane % 8, span) has rows row_lo + 8 k of
+// one 16-channel span, k = 0 .. 3, so that the span's key scales are read and paired once for four rows and
+// the eight lanes of a store phase hit eight rows, whose chunks lie in distinct banks under the swizzle.
+// st: the raw stage, already at the lane's place (row_lo, span) of each part; dst: the operand tile at row
+// row_lo of the subtile, a0 and a1 the lane's chunk offsets; gsh = log2 G.
+template <int KB, int VB, bool VALUES>
+__device__ __forceinline__ void fill_packed(const unsigned char* st, int gsh, int row_lo, int span, unsigned char* dst, uint32_t a0,
+                                            uint32_t a1) {
+    using Raw = RawLayout<KB, VB>;
+    constexpr int BITS = VALUES ? VB : KB;
     constexpr int kRowBytes = kD * BITS / 8, kSpanBytes = 2 * BITS;
+    const unsigned char* codes = st + (VALUES ? Raw::kVc : Raw::kKc) + row_lo * kRowBytes + span * kSpanBytes;
+    uint32_t sc[8], zr[8];
+    const unsigned char* meta = nullptr;
+    const int vsh = 8 - gsh;   // log2 of the bytes of a token's value scales, 2 D / G
+    if constexpr (!VALUES) {
+        auto row = [&](int at, uint32_t (&out)[8]) {
+            const uint4 a = *reinterpret_cast<const uint4*>(st + at + span * 32), b = *reinterpret_cast<const uint4*>(st + at + span * 32 + 16);
+            const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            pair_words<BITS>(x, out);
+        };
+        row(Raw::kKs, sc);
+        row(Raw::kKz, zr);
+    } else {
+        meta = st + Raw::kVs + (row_lo << vsh) + (((span * 16) >> gsh) << 1);
+    }
+    // two rows at a time: the roles' loops together have to fit the instruction cache (all four
+    // rows unrolled, and the other loops likewise, ran at about half the speed)
 #pragma unroll 1
-    for (int sub = 0; sub < kKeys / kTile; ++sub) {
-        const int64_t tb = t0 + sub * kTile;
-        uint32_t o[2][8];
-        if (tb < s.np) {
-            const GroupAddr g = tile_addr(*s.sq, a.H, h, tb / kTile, kD, a.kb, a.vb, a.G);
-            uint32_t sc[8], zr[8];
-            if constexpr (!VALUES) {
-                uint32_t w[8];
-                load8(w, g.ks + span * 16);
-                pair_words<BITS>(w, sc);
-                load8(w, g.kz + span * 16);
-                pair_words<BITS>(w, zr);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int row = row_lo + 16 * k;
-                const unsigned char* code = (VALUES ? g.vc : g.kc) + row * kRowBytes + span * kSpanBytes;
-                uint32_t w[BITS / 2];
-                if constexpr (BITS == 2) {
-                    w[0] = __ldg(reinterpret_cast<const uint32_t*>(code));
-                } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(code));
-                    w[0] = x.x;
-                    w[1] = x.y;
-                }
-                uint32_t c[8];
-                pair_codes<BITS>(w, c);
-                if constexpr (VALUES) {
-                    const int ng = kD / a.G, gr = span * 16 / a.G;
-                    const uint32_t s1 = __ldg(g.vs + row * ng + gr), z1 = __ldg(g.vz + row * ng + gr);
-                    const uint32_t s2 = prmt(s1, s1, 0x1010u), z2 = prmt(z1, z1, 0x1010u);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[k][i] = hfma2(c[i], s2, z2);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[k][i] = hfma2(c[i], sc[i], zr[i]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int64_t t = tb + row_lo + 16 * k;
-                uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};   // rows behind the last token: zeros
-                if (t < s.L) load8(w, s.res + (t % s.ring) * kD + span * 16);
-                else if (t < s.end) load8(w, s.fresh + (t - s.L) * kD + span * 16);
-                pair_stored<BITS, DT>(w, o[k]);
-            }
-        }
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int row = sub * kTile + row_lo + 16 * k;
-            *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span)) = make_uint4(o[k][0], o[k][1], o[k][2], o[k][3]);
-            *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span + 1)) = make_uint4(o[k][4], o[k][5], o[k][6], o[k][7]);
+            uint32_t w[BITS / 2], c[8];
+            const unsigned char* code = codes + 8 * k * kRowBytes;
+            if constexpr (BITS == 2) {
+                w[0] = *reinterpret_cast<const uint32_t*>(code);
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(code);
+                w[0] = x.x;
+                w[1] = x.y;
+            }
+            pair_codes<BITS>(w, c);
+            if constexpr (VALUES) {
+                const uint32_t s1 = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh));
+                const uint32_t z1 = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh) + (Raw::kVz - Raw::kVs));
+                const uint32_t s2 = prmt(s1, s1, 0x1010u), z2 = prmt(z1, z1, 0x1010u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], s2, z2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], sc[i], zr[i]);
+            }
+            *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(c[4], c[5], c[6], c[7]);
         }
+        codes += 16 * kRowBytes;
+        dst += 2048;
+        if constexpr (VALUES) meta += 16 << vsh;
+    }
+}
+
+// Stored tokens (the ring's and the chunk's own) of a kv head.
+struct ChunkStored {
+    const uint16_t *res, *fresh;
+    int L, end;   // cached tokens; cached and new ones
+    int ring;
+};
+// The four rows of a lane of the stored subtile at token tb; rows behind the last token are zeros.
+__device__ __forceinline__ void load_stored(const ChunkStored& s, int tb, int row_lo, int span, uint32_t (&w)[4][8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int t = tb + row_lo + 8 * k;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[k][i] = 0;
+        if (t < s.L) load8(w[k], s.res + static_cast<int64_t>(t % s.ring) * kD + span * 16);
+        else if (t < s.end) load8(w[k], s.fresh + static_cast<int64_t>(t - s.L) * kD + span * 16);
     }
 }
 
@@ -408,7 +475,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     unsigned char* sq_tile = smem;                                   // [2] query tiles
     unsigned char* sk_tile = smem + 2 * kOpBytes;                    // [kKvStages]
     unsigned char* sv_tile = sk_tile + kKvStages * kOpBytes;         // [kKvStages]
-    ChunkShared& sh = *reinterpret_cast<ChunkShared*>(sv_tile + kKvStages * kOpBytes);
+    using Raw = RawLayout<KB, VB>;
+    unsigned char* raw_ring = sv_tile + kKvStages * kOpBytes;        // [Raw::kStages] raw packed subtiles
+    ChunkShared& sh = *reinterpret_cast<ChunkShared*>(raw_ring + Raw::kStages * Raw::kBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
     const int g = a.Hq / a.H;
     volatile int* stop = &sh.stop;
@@ -437,6 +506,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             mbar_init(smem_u32(&sh.p_full[i]), 128);
             mbar_init(smem_u32(&sh.o_done[i]), 1);
         }
+        for (int i = 0; i < Raw::kStages; ++i) {
+            mbar_init(smem_u32(&sh.raw_full[i]), 1);
+            mbar_init(smem_u32(&sh.raw_empty[i]), 4);   // the warps that read a subtile
+        }
+        for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_u32(&sh.seg_full[i]), 1);
+            mbar_init(smem_u32(&sh.seg_empty[i]), kSegReaders);
+        }
+        mbar_init(smem_u32(&sh.hand_full), 128);
+        mbar_init(smem_u32(&sh.hand_empty), 128);
         sh.stop = 0;
         sh.idx = INT64_MAX;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -491,23 +570,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     }
     if (tid == 0) a.info[c].nseg = 0;
     __syncthreads();
-    ChunkWalk w;
-    w.lo = sh.lo; w.hi = sh.hi; w.pos = sh.pos; w.idx = sh.idx; w.U = sh.U; w.C = sh.C; w.h = sh.h;
-    ChunkSeg s;
     const uint32_t tmem = sh.tmem;
+    bool ok = true;
+    // segment i of this CTA in sh.seg: whether there is one, and the word that this warp is done with it
+    auto seg_next = [&](uint32_t i) {
+        ok = mbar_wait(smem_u32(&sh.seg_full[i % kSegs]), (i / kSegs) & 1, stop);
+        return ok && sh.seg[i % kSegs].x1 > 0;
+    };
+    auto seg_done = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[i % kSegs]));
+    };
 
     if (warp < kChunkSoftmaxWarps) {
-        // ------------------------------------------------ softmax of one row tile
-        const int tile = warp >> 2, r = tid & 127;
+        // ------------------------------------------------ softmax
+        // Wide segments: warpgroup t has row tile t. Narrow ones (at most 128 rows): both have the one row
+        // tile, and take its key tiles in turn, each with its own state and output columns, joined at the end.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int wg = warp >> 2, r = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;     // this warp's 32 TMEM lanes
-        const uint32_t t_s = tmem + lane_off + tile * kKeys, t_o = tmem + lane_off + 2 * kKeys + tile * kD;
-        unsigned char* qt = sq_tile + tile * kOpBytes;
-        uint32_t ns = 0, nq = 0;    // score tiles and segments so far
-        bool ok = true;
-        while (ok && chunk_next(a, w, s)) {
-            if (tile * kRows >= s.it.rows) continue;   // this row tile is empty
+        const uint32_t t_s = tmem + lane_off + wg * kKeys, t_o = tmem + lane_off + 2 * kKeys + wg * kD;
+        uint32_t ns = 0, nq = 0, nh = 0;    // score tiles, segments and handed states so far
+        for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+            const ChunkSeg& s = sh.seg[si % kSegs];
+            const bool narrow = s.it.rows <= kRows;
+            const int tile = narrow ? 0 : wg, step = narrow ? 2 : 1;
             const int row = s.it.row0 + tile * kRows + r;
             const bool live = tile * kRows + r < s.it.rows;
+            const bool warp_live = tile * kRows + (r & ~31) < s.it.rows;     // some row of this warp is real
             const int qi = row / g;
             const int64_t qrow = (static_cast<int64_t>(a.q_start[s.it.b]) + qi) * a.Hq + s.h * g + (row - qi * g);
             float sl;                                    // log2 units per score
@@ -528,129 +618,192 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                 if (mx > 0.0f && a.scale_log2 != 0.0f) frexpf(mx, &e);
                 const float pre = a.scale_log2 == 0.0f ? 0.0f : copysignf(ldexpf(1.0f, -e), a.scale_log2);
                 sl = a.scale_log2 == 0.0f ? 1.0f : ldexpf(fabsf(a.scale_log2), e);
+                if (wg == tile) {
+                    unsigned char* qt = sq_tile + tile * kOpBytes;
 #pragma unroll 2
-                for (int sp = 0; sp < 8; ++sp) {
-                    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
-                    if (live) load8(x, q + sp * 16);
+                    for (int sp = 0; sp < 8; ++sp) {
+                        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
+                        if (live) load8(x, q + sp * 16);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int c0 = span_channel<KB>(2 * i), c1 = span_channel<KB>(2 * i + 1);
-                        const float x0 = widen<DT>(static_cast<uint16_t>((c0 & 1) ? x[c0 >> 1] >> 16 : x[c0 >> 1]));
-                        const float x1 = widen<DT>(static_cast<uint16_t>((c1 & 1) ? x[c1 >> 1] >> 16 : x[c1 >> 1]));
-                        o[i] = pack_h2(x0 * pre, x1 * pre);
+                        for (int i = 0; i < 8; ++i) {
+                            const int c0 = span_channel<KB>(2 * i), c1 = span_channel<KB>(2 * i + 1);
+                            const float x0 = widen<DT>(static_cast<uint16_t>((c0 & 1) ? x[c0 >> 1] >> 16 : x[c0 >> 1]));
+                            const float x1 = widen<DT>(static_cast<uint16_t>((c1 & 1) ? x[c1 >> 1] >> 16 : x[c1 >> 1]));
+                            o[i] = pack_h2(x0 * pre, x1 * pre);
+                        }
+                        store_rows(qt, r, sp, o);
                     }
-                    *reinterpret_cast<uint4*>(qt + op_addr(r, 2 * sp)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(qt + op_addr(r, 2 * sp + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    proxy_fence();
+                    mbar_arrive(smem_u32(&sh.q_full[tile]));
                 }
-                proxy_fence();
-                mbar_arrive(smem_u32(&sh.q_full[tile]));
             }
             // tokens this row sees: [lo, pos] and [0, sinks)
-            const int64_t pos = s.it.L + qi;
-            const int64_t lo = a.window > 0 ? pos + 1 - a.window : 0;
-            const int64_t snk = a.window > 0 ? a.sinks : 0;
-            const int64_t tile_first = s.it.L + (s.it.row0 + tile * kRows) / g;   // position of the row tile's first query
-            const int64_t tile_last = s.it.L + (s.it.row0 + tile * kRows + kRows - 1) / g;
+            const int len = static_cast<int>(s.it.L), pos = len + qi;
+            const int lo = a.window > 0 ? pos + 1 - a.window : 0;
+            const int snk = a.window > 0 ? a.sinks : 0;
+            const int tile_first = len + (s.it.row0 + tile * kRows) / g;   // position of the row tile's first query
+            const int tile_last = len + (s.it.row0 + tile * kRows + kRows - 1) / g;
 
             float m = -CUDART_INF_F, l = 0.0f;
-            for (int j = s.x0; j < s.x1; ++j) {
-                ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.s_full[tile]), ns & 1, stop));
+            const int j0 = s.x0 + (narrow ? wg : 0);
+            for (int j = j0; j < s.x1; j += step) {
+                ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.s_full[wg]), ns & 1, stop));
                 if (!ok) break;
                 ++ns;
-                tc_fence_after();
-                const int64_t t0 = static_cast<int64_t>(j < s.it.st ? j : j + s.it.skip) * kKeys;
-                const bool cut = t0 + kKeys - 1 > tile_first ||
-                                 (a.window > 0 && t0 <= tile_last - a.window && t0 + kKeys > a.sinks);
-                // the row's bounds inside this tile: columns [c_lo, c_hi) and [0, c_snk)
-                const int c_hi = static_cast<int>(pos + 1 - t0 < kKeys ? pos + 1 - t0 : kKeys);
-                const int c_lo = static_cast<int>(lo - t0 > 0 ? (lo - t0 < kKeys ? lo - t0 : kKeys) : 0);
-                const int c_snk = static_cast<int>(snk - t0 > 0 ? (snk - t0 < kKeys ? snk - t0 : kKeys) : 0);
-                auto mask = [&](float (&x)[32], int c0) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c0 + i >= c_hi || (c0 + i < c_lo && c0 + i >= c_snk)) x[i] = -CUDART_INF_F;
-                };
-                float mx = -CUDART_INF_F;
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) {
-                    float x[32];
-                    tc_ld32(x, t_s + 32 * q);
-                    tc_wait_ld();
-                    if (cut) mask(x, 32 * q);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
+                if (!warp_live) {     // no row to serve: its products go nowhere
+                    mbar_arrive(smem_u32(&sh.p_full[wg]));
+                    continue;
                 }
-                mx *= sl;
-                const bool grow = mx > m + kLag || (m == -CUDART_INF_F && mx > m);
+                tc_fence_after();
+                const int t0 = (j < s.it.st ? j : j + s.it.skip) * kKeys;
+                const bool cut = t0 + kKeys - 1 > tile_first ||
+                                 (a.window > 0 && t0 <= tile_last - a.window && t0 + kKeys > snk);
+                // the row's bounds inside this tile: columns [c_lo, c_hi) and [0, c_snk)
+                const int c_hi = pos + 1 - t0, c_lo = lo - t0, c_snk = snk - t0;
+                // Both passes go by 64 columns in loops that are not unrolled: the roles of this kernel run different
+                // code at the same time, and with everything unrolled they waited for instructions.
+                auto mask = [&](float (&y)[2][32], int c0) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (c0 + i >= c_hi || (c0 + i < c_lo && c0 + i >= c_snk)) y[i >> 5][i & 31] = -CUDART_INF_F;
+                };
+                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                for (int q = 0; q < kKeys; q += 64) {
+                    float x[2][32];
+                    tc_ld32(x[0], t_s + q);
+                    tc_ld32(x[1], t_s + q + 32);
+                    tc_wait_ld();
+                    if (__builtin_expect(cut, 0)) mask(x, q);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], fmaxf(x[i >> 4][2 * (i & 15)], x[i >> 4][2 * (i & 15) + 1]));
+                }
+                const float top = fmaxf(mx[0], mx[1]) * sl;
+                const bool grow = m == -CUDART_INF_F ? top > m : top > m + kLag;
                 if (__any_sync(kFull, grow)) {
-                    const float mn = grow ? mx : m;
-                    const float alpha = grow ? exp2_ftz(m - mn) : 1.0f;     // 0 while m is -inf
+                    const float alpha = grow ? exp2_ftz(m - top) : 1.0f;     // 0 while m is -inf
                     l *= alpha;
-                    m = mn;
-                    if (j > s.x0) {     // the products of the tiles before are complete (they precede these scores)
+                    if (grow) m = top;
+                    if (j > j0) {     // the products of the tiles before are complete (they precede these scores)
 #pragma unroll 1
                         for (int q = 0; q < kD / 32; ++q) {
-                            float x[32];
-                            tc_ld32(x, t_o + 32 * q);
+                            float y[32];
+                            tc_ld32(y, t_o + 32 * q);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] *= alpha;
-                            tc_st32(t_o + 32 * q, x);
+                            for (int i = 0; i < 32; ++i) y[i] *= alpha;
+                            tc_st32(t_o + 32 * q, y);
                         }
                         tc_wait_st();
                     }
                 }
                 const float mref = m == -CUDART_INF_F ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int q = 0; q < kKeys / 32; ++q) {
-                    float x[32];
-                    tc_ld32(x, t_s + 32 * q);
+                const float2 sl2 = make_float2(sl, sl), mn2 = make_float2(-mref, -mref);
+                float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+                for (int q = 0; q < kKeys; q += 64) {
+                    float x[2][32];
+                    tc_ld32(x[0], t_s + q);
+                    tc_ld32(x[1], t_s + q + 32);
                     tc_wait_ld();
-                    if (cut) mask(x, 32 * q);
-                    uint32_t p[16];
+                    if (__builtin_expect(cut, 0)) mask(x, q);
+                    float p[32];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float p0 = exp2_ftz(fmaf(x[2 * i], sl, -mref)), p1 = exp2_ftz(fmaf(x[2 * i + 1], sl, -mref));
-                        sum[i & 3] += p0 + p1;
-                        p[i] = pack_h2(p0, p1);
+                    for (int i = 0; i < 32; ++i) {
+                        float2 e = fma2(make_float2(x[i >> 4][2 * (i & 15)], x[i >> 4][2 * (i & 15) + 1]), sl2, mn2);
+                        e.x = exp2_ftz(e.x);
+                        e.y = exp2_ftz(e.y);
+                        acc[i & 1] = add2(acc[i & 1], e);
+                        p[i] = __uint_as_float(pack_h2(e.x, e.y));
                     }
-                    tc_st16(t_s + 16 * q, p);
+                    tc_st32(t_s + (q >> 1), p);   // over scores that have been read
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                acc[0] = add2(acc[0], acc[1]);
+                l += acc[0].x + acc[0].y;
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[tile]));
+                mbar_arrive(smem_u32(&sh.p_full[wg]));
             }
-            ok = ok && __all_sync(kFull, mbar_wait(smem_u32(&sh.o_done[tile]), nq & 1, stop));
-            if (!ok) break;
-            ++nq;
-            tc_fence_after();
-            const bool whole = s.x0 == 0 && s.x1 == s.it.nt;
-            const float inv = whole ? 1.0f / l : 1.0f;
-            float* rec = whole ? nullptr : chunk_record(a, 2 * static_cast<int64_t>(c) + (s.x0 == 0), tile);
-#pragma unroll 1
-            for (int q = 0; q < kD / 32; ++q) {
-                float x[32], y[32];
-                tc_ld32(x, t_o + 32 * q);
-                tc_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) y[(i & 16) + span_channel<VB>(i & 15)] = x[i] * inv;
-                if (live && whole) {
-                    store32<DT>(a.out, qrow, 32 * q, y);
-                } else if (live) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4*>(rec)[(8 * q + i) * kRows + r] =
-                            make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            const bool any = j0 < s.x1;      // this warpgroup had tiles
+            if (any) {
+                ok = ok && __all_sync(kFull, mbar_wait(smem_u32(&sh.o_done[wg]), nq & 1, stop));
+                if (!ok) break;
+                ++nq;
+                tc_fence_after();
+            }
+            float f0 = 1.0f, f1 = 0.0f;      // factors of the two states of a narrow segment
+            bool both = false;
+            if (narrow && s.x1 - s.x0 > 1) {
+                if (wg == 1) {
+                    // hand the state over; the output columns are read from TMEM by the other warpgroup
+                    sh.hand_m[r] = m;
+                    sh.hand_l[r] = l;
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&sh.hand_full));
+                    ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.hand_empty), nh & 1, stop));
+                    ++nh;
+                    tc_fence_after();
+                    continue;
                 }
-                __syncwarp();
+                ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.hand_full), nh & 1, stop));
+                if (!ok) break;
+                ++nh;
+                tc_fence_after();
+                both = true;
+                const float m1 = sh.hand_m[r], l1 = sh.hand_l[r], mt = fmaxf(m, m1);
+                if (mt != -CUDART_INF_F) {
+                    f0 = exp2_ftz(m - mt);
+                    f1 = exp2_ftz(m1 - mt);
+                }
+                l = l * f0 + l1 * f1;
+                m = mt;
+            } else if (narrow && wg == 1) {
+                continue;
+            }
+            const bool whole = s.x0 == 0 && s.x1 == s.it.nt;
+            if (whole) {
+                const float inv = 1.0f / l;
+                f0 *= inv;
+                f1 *= inv;
+            }
+            float* rec = whole ? nullptr : chunk_record(a, 2 * static_cast<int64_t>(c) + (s.x0 == 0), tile);
+            if (warp_live) {
+#pragma unroll 1
+                for (int q = 0; q < kD / 32; ++q) {
+                    float x[32], y[32];
+                    tc_ld32(x, t_o + 32 * q);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[(i & 16) + span_channel<VB>(i & 15)] = x[i] * f0;
+                    if (both) {
+                        tc_ld32(x, t_o + kD + 32 * q);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float& z = y[(i & 16) + span_channel<VB>(i & 15)];
+                            z = fmaf(x[i], f1, z);
+                        }
+                    }
+                    if (live && whole) {
+                        store32<DT>(a.out, qrow, 32 * q, y);
+                    } else if (live) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<float4*>(rec)[(8 * q + i) * kRows + r] =
+                                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (both) {
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.hand_empty));
             }
             if (!whole && live) {
                 rec[kRows * kD + r] = m;
                 rec[kRows * kD + kRows + r] = l;
             }
-            if (!whole && s.x0 == 0 && r == 0 && tile == 0) {
+            if (!whole && s.x0 == 0 && tid == 0) {
                 ChunkInfo f;
                 f.b = s.it.b;
                 f.row0 = s.it.row0;
@@ -663,81 +816,227 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
         }
     } else if (warp < 16) {
         // ------------------------------------------------ keys (warps 8-11) and values (12-15)
-        const bool keys = warp < 12;
-        const int p = tid & 127;
-        uint64_t* full = keys ? sh.k_full : sh.v_full;
-        uint64_t* empty = keys ? sh.k_empty : sh.v_empty;
-        unsigned char* tiles = keys ? sk_tile : sv_tile;
-        uint32_t n = 0;
-        bool ok = true;
-        while (ok && chunk_next(a, w, s)) {
-            ChunkSrc src;
-            const kivi_seq& sq = a.seqs[s.it.b];
-            src.sq = &sq;
-            src.L = s.it.L;
-            src.np = n_packed(s.it.L, a.R, a.G);
-            src.end = s.it.L + s.it.n;
-            src.ring = a.R + a.G;
-            src.res = static_cast<const uint16_t*>(keys ? sq.k_res : sq.v_res) + static_cast<int64_t>(s.h) * src.ring * kD;
-            src.fresh = static_cast<const uint16_t*>(keys ? a.k_new[s.it.b] : a.v_new[s.it.b]) +
-                        static_cast<int64_t>(s.h) * s.it.n * kD;
-            for (int j = s.x0; j < s.x1; ++j, ++n) {
-                const uint32_t st = n % kKvStages, use = n / kKvStages;
-                if (use > 0 && !mbar_wait(smem_u32(&empty[st]), (use - 1) & 1, stop)) { ok = false; break; }
-                const int64_t t0 = static_cast<int64_t>(j < s.it.st ? j : j + s.it.skip) * kKeys;
-                if (keys) fill_tile<KB, DT, false>(a, src, s.h, t0, tiles + st * kOpBytes, p);
-                else fill_tile<VB, DT, true>(a, src, s.h, t0, tiles + st * kOpBytes, p);
-                proxy_fence();
-                mbar_arrive(smem_u32(&full[st]));
-            }
-        }
-    } else if (lane == 0) {
-        // ------------------------------------------------ tensor-core issue
-        uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};   // key tiles, probability tiles, segments so far
-        bool ok = true;
-        const uint32_t kb0 = smem_u32(sk_tile), vb0 = smem_u32(sv_tile), qb0 = smem_u32(sq_tile);
-        auto scores = [&](int t, uint32_t st) {
-            const uint32_t q = qb0 + t * kOpBytes, k = kb0 + st * kOpBytes;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOperandRegs));
+        auto operands = [&](auto values) {
+            constexpr bool VALUES = decltype(values)::value;
+            constexpr int BITS = VALUES ? VB : KB;
+            // warps 0 and 1 of the group take the even subtiles of a tile, 2 and 3 the odd ones; each warp has
+            // half of the spans
+            const int odd = (warp >> 1) & 1, row_lo = lane & 7, span = (lane >> 3) + 4 * (warp & 1);
+            const uint32_t a0 = op_addr(row_lo, 2 * span), a1 = op_addr(row_lo, 2 * span + 1);
+            const int gsh = a.G == 64 ? 6 : 5;
+            uint64_t* full = VALUES ? sh.v_full : sh.k_full;
+            uint64_t* empty = VALUES ? sh.v_empty : sh.k_empty;
+            unsigned char* tiles = VALUES ? sv_tile : sk_tile;
+            uint32_t n = 0, raw0 = 0, raw_par = 0;    // tiles so far; stage and parity of the tile's first raw subtile
+            for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+                const ChunkSeg& s = sh.seg[si % kSegs];
+                const kivi_seq& sq = a.seqs[s.it.b];
+                const int np = static_cast<int>(n_packed(s.it.L, a.R, a.G));
+                ChunkStored src;
+                src.L = static_cast<int>(s.it.L);
+                src.end = src.L + s.it.n;
+                src.ring = a.R + a.G;
+                src.res = static_cast<const uint16_t*>(VALUES ? sq.v_res : sq.k_res) + static_cast<int64_t>(s.h) * src.ring * kD;
+                src.fresh = static_cast<const uint16_t*>(VALUES ? a.v_new[s.it.b] : a.k_new[s.it.b]) +
+                            static_cast<int64_t>(s.h) * s.it.n * kD;
+                const int x1 = s.x1, lst = s.it.st, skip = s.it.skip;
+                for (int j = s.x0; j < x1; ++j, ++n) {
+                    const uint32_t st = n % kKvStages, use = n / kKvStages;
+                    const int t0 = (j < lst ? j : j + skip) * kKeys;
+                    const int packed = np <= t0 ? 0 : np - t0 >= kKeys ? kKeys / kTile : (np - t0) / kTile;   // subtiles
+                    auto wait_empty = [&]() {
+                        if (use > 0) ok = __all_sync(kFull, mbar_wait(smem_u32(&empty[st]), (use - 1) & 1, stop));
+                    };
+                    unsigned char* dst = tiles + st * kOpBytes + odd * (kTile * 128);
+                    auto stored = [&](const uint32_t (&x)[4][8], unsigned char* to) {
 #pragma unroll
-            for (int i = 0; i < kD / 16; ++i) {
-                const uint32_t off = (i >> 2) * (kRows * 128) + (i & 3) * 32;
-                mma_ss(tmem + t * kKeys, op_desc(q + off, 16, 1024), op_desc(k + off, 16, 1024), kIdescQK, i > 0);
-            }
-            tc_commit(smem_u32(&sh.s_full[t]));
-        };
-        while (ok && chunk_next(a, w, s)) {
-            const int nt = s.it.rows > kRows ? 2 : 1, cnt = s.x1 - s.x0;
-            for (int t = 0; t < nt && ok; ++t) {
-                ok = mbar_wait(smem_u32(&sh.q_full[t]), nq[t] & 1, stop);
-                ++nq[t];
-            }
-            ok = ok && mbar_wait(smem_u32(&sh.k_full[n % kKvStages]), (n / kKvStages) & 1, stop);
-            if (!ok) break;
-            tc_fence_after();
-            for (int t = 0; t < nt; ++t) scores(t, n % kKvStages);
-            tc_commit(smem_u32(&sh.k_empty[n % kKvStages]));
-            for (int j = 0; j < cnt; ++j, ++n) {
-                const uint32_t st = n % kKvStages, par = (n / kKvStages) & 1;
-                const uint32_t st1 = (n + 1) % kKvStages, par1 = ((n + 1) / kKvStages) & 1;
-                const bool more = j + 1 < cnt;
-                ok = mbar_wait(smem_u32(&sh.v_full[st]), par, stop) &&
-                     (!more || mbar_wait(smem_u32(&sh.k_full[st1]), par1, stop));
-                for (int t = 0; t < nt && ok; ++t) {
-                    ok = mbar_wait(smem_u32(&sh.p_full[t]), np[t] & 1, stop);
-                    if (!ok) break;
-                    ++np[t];
-                    tc_fence_after();
-                    const uint32_t v = vb0 + st * kOpBytes;
-#pragma unroll
-                    for (int i = 0; i < kKeys / 16; ++i)
-                        mma_ts(tmem + 2 * kKeys + t * kD, tmem + t * kKeys + 8 * i, op_desc(v + i * 2048, kRows * 128, 1024),
-                               kIdescPV, j > 0 || i > 0);
-                    if (more) scores(t, st1);
-                    else tc_commit(smem_u32(&sh.o_done[t]));
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t o[8];
+                            pair_stored<BITS, DT>(x[k], o);
+                            *reinterpret_cast<uint4*>(to + a0 + 1024 * k) = make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4*>(to + a1 + 1024 * k) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    };
+                    if (odd < packed) {
+                        wait_empty();
+                        if (!ok) break;
+#pragma unroll 1
+                        for (int sub = odd; sub < packed; sub += 2, dst += 2 * kTile * 128) {
+                            const bool wrap = raw0 + sub >= Raw::kStages;
+                            const uint32_t slot = wrap ? raw0 + sub - Raw::kStages : raw0 + sub;
+                            ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.raw_full[slot]), raw_par ^ wrap, stop));
+                            if (!ok) break;
+                            fill_packed<KB, VB, VALUES>(raw_ring + slot * Raw::kBytes, gsh, row_lo, span, dst, a0, a1);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[slot]));
+                        }
+                        if (!ok) break;
+                        if (odd + 2 >= packed) {     // the tile's second half is stored tokens
+                            uint32_t x[4][8];
+                            load_stored(src, t0 + (odd + 2) * kTile, row_lo, span, x);
+                            stored(x, dst);
+                        }
+                    } else {
+                        uint32_t x[4][8];
+                        load_stored(src, t0 + odd * kTile, row_lo, span, x);
+                        wait_empty();
+                        if (!ok) break;
+                        stored(x, dst);
+                        load_stored(src, t0 + (odd + 2) * kTile, row_lo, span, x);
+                        stored(x, dst + 2 * kTile * 128);
+                    }
+                    raw0 += packed;
+                    if (raw0 >= Raw::kStages) {
+                        raw0 -= Raw::kStages;
+                        raw_par ^= 1;
+                    }
+                    proxy_fence();
+                    mbar_arrive(smem_u32(&full[st]));
                 }
-                if (!ok) break;
-                tc_commit(smem_u32(&sh.v_empty[st]));
-                if (more) tc_commit(smem_u32(&sh.k_empty[st1]));
+            }
+        };
+        if (warp < 12) operands(std::integral_constant<bool, false>{});
+        else operands(std::integral_constant<bool, true>{});
+    } else if (warp == 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        // ------------------------------------------------ tensor-core issue: the whole warp walks, one lane issues
+        uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};   // key tiles, probability tiles, segments so far
+        const uint32_t kb0 = smem_u32(sk_tile), vb0 = smem_u32(sv_tile), qb0 = smem_u32(sq_tile);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = __all_sync(kFull, mbar_wait(smem_u32(bar), parity, stop));
+            return ok;
+        };
+        for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+            // A segment is a row of events: event e is key tile j(e) for the softmax warpgroup t = e & 1. Wide: both
+            // warpgroups (row tiles) take every tile, e = 2 j + t; narrow: they take tiles in turn, e = j. Two
+            // score products run ahead; after the products of event e its S is free for the scores of e + 2. One
+            // rolled loop for both: the issuing code has to stay small to stay cached.
+            const int narrow = sh.seg[si % kSegs].it.rows <= kRows;
+            const int cnt = sh.seg[si % kSegs].x1 - sh.seg[si % kSegs].x0, events = narrow ? cnt : 2 * cnt;
+            const int wide = 1 - narrow;
+            if (!wait(&sh.q_full[0], nq[0]++ & 1)) break;
+            if (wide && !wait(&sh.q_full[1], nq[1]++ & 1)) break;
+#pragma unroll 1
+            for (int e = -2; e < events; ++e) {
+                const uint32_t t = e & 1;
+                if (e >= 0) {
+                    const uint32_t u = n + (e >> wide), st = u % kKvStages;
+                    if (!wait(&sh.v_full[st], (u / kKvStages) & 1)) break;
+                    if (!wait(&sh.p_full[t], (t ? np[1]++ : np[0]++) & 1)) break;
+                    tc_fence_after();
+                    // (broadcast, so that the compiler keeps the operands in uniform registers)
+                    const uint32_t v = __shfl_sync(kFull, desc_lo(vb0 + st * kOpBytes, kRows * 128), 0);
+                    const uint32_t d = __shfl_sync(kFull, tmem + 2 * kKeys + t * kD, 0), p = __shfl_sync(kFull, tmem + t * kKeys, 0);
+                    const uint32_t acc = __shfl_sync(kFull, e > 1 ? 1u : 0u, 0);
+                    if (elect_one()) {
+                        mma_ts(d, p, v, kIdescPV, acc);
+#pragma unroll
+                        for (uint32_t i = 1; i < kKeys / 16; ++i) mma_ts(d, p + 8 * i, v + i * (2048 >> 4), kIdescPV, 1);
+                        if (narrow || t) tc_commit(smem_u32(&sh.v_empty[st]));
+                        if (e + 2 >= events) tc_commit(smem_u32(&sh.o_done[t]));
+                    }
+                }
+                if (e + 2 < events) {
+                    const uint32_t u = n + ((e + 2) >> wide), st = u % kKvStages;
+                    if (!wait(&sh.k_full[st], (u / kKvStages) & 1)) break;
+                    tc_fence_after();
+                    const uint32_t q = __shfl_sync(kFull, desc_lo(qb0 + wide * t * kOpBytes, 16), 0);
+                    const uint32_t k = __shfl_sync(kFull, desc_lo(kb0 + st * kOpBytes, 16), 0), d = __shfl_sync(kFull, tmem + t * kKeys, 0);
+                    if (elect_one()) {
+#pragma unroll
+                        for (uint32_t i = 0; i < kD / 16; ++i) {
+                            const uint32_t off = (i >> 2) * ((kRows * 128) >> 4) + (i & 3) * 2;
+                            mma_ss(d, q + off, k + off, kIdescQK, i > 0);
+                        }
+                        tc_commit(smem_u32(&sh.s_full[t]));
+                        if (narrow || t) tc_commit(smem_u32(&sh.k_empty[st]));
+                    }
+                }
+                __syncwarp();
+            }
+            n += cnt;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == 17) {
+            // -------------------------------------------- raw packed subtiles: lane i < 6 copies buffer i
+            uint32_t slot = 0, par = 0;
+            bool full_turn = false;
+            // Buffer of this lane: its bytes per subtile, its place in a raw stage, and the strides of a group
+            // and of a subtile within it.
+            const int nv = kD / a.G, tpg = a.G / kTile, bits = lane == 0 ? KB : VB;
+            const bool codes = lane == 0 || lane == 3, vmeta = lane > 3;
+            const uint32_t len = codes ? kTile * kD * bits / 8 : vmeta ? kTile * nv * 2 : kD * 2;
+            const uint32_t sub_stride = codes || vmeta ? len : 0, group_stride = sub_stride != 0 ? sub_stride * tpg : kD * 2;
+            const uint32_t at = lane == 0 ? Raw::kKc : lane == 1 ? Raw::kKs : lane == 2 ? Raw::kKz
+                              : lane == 3 ? Raw::kVc : lane == 4 ? Raw::kVs : Raw::kVz;
+            const uint32_t bytes = kTile * kD * (KB + VB) / 8 + 2 * kD * 2 + 2 * kTile * nv * 2;
+            for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+                const ChunkSeg& s = sh.seg[si % kSegs];
+                const kivi_seq& sq = a.seqs[s.it.b];
+                const unsigned char* base = static_cast<const unsigned char*>(
+                    lane == 0 ? static_cast<const void*>(sq.k_codes) : lane == 1 ? sq.k_scale : lane == 2 ? sq.k_zero
+                    : lane == 3 ? static_cast<const void*>(sq.v_codes) : lane == 4 ? sq.v_scale : sq.v_zero);
+                const bool paged = seq_paged(sq);
+                const int32_t* table = sq.block_table;
+                const int h = s.h, x1 = s.x1, st = s.it.st, skip = s.it.skip;
+                const int tiles = static_cast<int>(n_packed(s.it.L, a.R, a.G) / kTile);   // packed subtiles
+                const int64_t head = static_cast<int64_t>(h) * (sq.cap_tokens / a.G);     // contiguous: first group of the head
+                // pages ahead: lane i holds the page of group page0 + i
+                int page0 = -64, pages = 0;
+                for (int j = s.x0; ok && j < x1; ++j) {
+                    const int t0 = (j < st ? j : j + skip) * (kKeys / kTile);
+                    for (int t = t0; t < t0 + kKeys / kTile && t < tiles; ++t) {
+                        const int group = tpg == 1 ? t : t >> 1;
+                        int64_t at_group = head + group;
+                        if (paged) {
+                            if (group < page0 || group >= page0 + 32) {
+                                page0 = group;
+                                pages = (page0 + lane) * tpg < tiles ? __ldg(table + page0 + lane) : 0;
+                            }
+                            at_group = static_cast<int64_t>(__shfl_sync(kFull, pages, group - page0)) * a.H + h;
+                        }
+                        if (full_turn) ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.raw_empty[slot]), par ^ 1, stop));
+                        if (!ok) break;
+                        const uint32_t bar = smem_u32(&sh.raw_full[slot]);
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                        __syncwarp();
+                        if (lane < 6)
+                            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                                         ::"r"(smem_u32(raw_ring + slot * Raw::kBytes) + at),
+                                         "l"(base + at_group * group_stride + (tpg == 1 ? 0 : t & 1) * sub_stride), "r"(len), "r"(bar)
+                                         : "memory");
+                        if (++slot == Raw::kStages) {
+                            slot = 0;
+                            par ^= 1;
+                            full_turn = true;
+                        }
+                    }
+                }
+            }
+            // copies in flight land before the CTA ends (they have all been waited for, unless a wait ran out)
+            if (*stop != 0) {
+                const long long t1 = clock64();
+                for (uint32_t i = 0; i < Raw::kStages; ++i) {
+                    const uint32_t q = i < slot ? par : par ^ 1;    // parity of this stage's last use
+                    if (i >= slot && !full_turn) continue;
+                    while (!mbar_try(smem_u32(&sh.raw_full[i]), q) && clock64() - t1 < 4000000000LL) {}
+                }
+            }
+        } else if (warp == 18 && lane == 0) {
+            // -------------------------------------------- the walk over this CTA's share; x1 = 0 ends it
+            ChunkWalk w;
+            w.lo = sh.lo; w.hi = sh.hi; w.pos = sh.pos; w.idx = sh.idx; w.U = sh.U; w.C = sh.C; w.h = sh.h;
+            bool more = true;
+            for (uint32_t i = 0; more; ++i) {
+                ChunkSeg s;
+                more = chunk_next(a, w, s);
+                if (!more) s.x0 = s.x1 = 0;
+                if (i >= kSegs && !mbar_wait(smem_u32(&sh.seg_empty[i % kSegs]), (i / kSegs - 1) & 1, stop)) break;
+                sh.seg[i % kSegs] = s;
+                mbar_arrive(smem_u32(&sh.seg_full[i % kSegs]));
             }
         }
     }
@@ -809,13 +1108,13 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(ChunkArgs a) {
 // SMs of the current device, at most kChunkMaxCtas (one CTA each). The first launch of an
 // instantiation on a device raises its shared memory limit.
 template <typename K>
-int chunk_ctas(K kernel, std::atomic<int>* cache) {
+int chunk_ctas(K kernel, int smem, std::atomic<int>* cache) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
     const int have = cache[dev].load(std::memory_order_relaxed);
     if (have > 0) return have;
     int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChunkSmem) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     n = n > kChunkMaxCtas ? kChunkMaxCtas : n;
     cache[dev].store(n, std::memory_order_relaxed);
@@ -825,9 +1124,9 @@ int chunk_ctas(K kernel, std::atomic<int>* cache) {
 template <int KB, int VB, int DT>
 cudaError_t launch_chunk_dt(ChunkArgs a, cudaStream_t stream) {
     static std::atomic<int> ctas[kMaxDevices];
-    a.ctas = chunk_ctas(chunk_kernel<KB, VB, DT>, ctas);
+    a.ctas = chunk_ctas(chunk_kernel<KB, VB, DT>, chunk_smem<KB, VB>(), ctas);
     if (a.ctas <= 0) return cudaErrorInvalidValue;
-    chunk_kernel<KB, VB, DT><<<a.ctas, kChunkThreads, kChunkSmem, stream>>>(a);
+    chunk_kernel<KB, VB, DT><<<a.ctas, kChunkThreads, chunk_smem<KB, VB>(), stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
