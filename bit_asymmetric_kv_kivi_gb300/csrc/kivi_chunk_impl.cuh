@@ -10,10 +10,14 @@
 //                    online softmax, probabilities back to TMEM as f16, output epilogue
 //   warps 8-11       keys: codes, scales and zeros (or stored rows) to an f16 tile in shared memory
 //   warps 12-15      values, the same
-//   warp 16          issues tcgen05.mma (kind::f16, M = N = 128): S = Q K^T from shared memory, O += P V
-//                    with P from TMEM
-// TMEM: S0, S1 (128 columns each, P over the first 64 of S), O0, O1. While the softmax of one row
-// tile runs, the tensor core works on the other.
+//   warps 16, 19     issue tcgen05.mma (kind::f16, M = N = 128), one for each softmax warpgroup: S = Q K^T from
+//                    shared memory, O += P V with P from TMEM
+//   warp 17          brings packed tokens into shared memory; warp 18 walks the CTA's work
+// TMEM: for each row tile two score buffers of 64 tokens (64 columns, P over the first 32) and the
+// output (128 columns). While the softmax works on one half of a key tile, the tensor core
+// makes the scores of the next half and the other row tile's products: with one 128-token
+// buffer per row tile, scores, softmax and products of a tile ran one after the other and took
+// 5200 clocks a tile, against 2140 that the tensor core needs for both row tiles.
 //
 // Rounding: operands are f16 whatever the storage type. A dequantized token is rounded once,
 // fma(c, s, z) to 11 bits, as an f16 cache would hold it; stored bf16 tokens with |x| <= 65504 are
@@ -41,11 +45,16 @@ constexpr int kChunkSoftmaxWarps = 8;
 constexpr int kChunkThreads = 20 * 32;
 constexpr int kRows = 128;                // rows of a row tile
 constexpr int kKeys = 128;                // tokens of a key tile
+constexpr int kHalf = 64;                 // tokens of a score buffer
 constexpr int kOpBytes = kRows * kD * 2;  // one 128 x 128 f16 operand tile
 constexpr int kKvStages = 2;
 // Registers per thread of the softmax, operand and issue warpgroups: setmaxnreg moves them from
-// the launch's 96 x 640, and the three shares add up to it (256 x 152 + 256 x 72 + 128 x 32).
+// the launch's 96 x 640, and the three shares add up to it.
 constexpr int kSoftmaxRegs = 120, kOperandRegs = 88, kIssueRegs = 64;
+constexpr int kLaunchRegs = 96;           // what the launch bounds leave a thread
+static_assert(kSoftmaxRegs >= kLaunchRegs && kOperandRegs <= kLaunchRegs && kIssueRegs <= kLaunchRegs,
+              "setmaxnreg.inc must not lower a count, nor setmaxnreg.dec raise one");
+static_assert(256 * kSoftmaxRegs + 256 * kOperandRegs + 128 * kIssueRegs <= kChunkThreads * kLaunchRegs, "shares of the launch's registers");
 constexpr int kUnitOverhead = 3;          // units charged per (row tile pair, kv head)
 constexpr int kMinChunkUnits = 4;
 constexpr float kLag = 8.0f;              // log2 by which the softmax reference may lag behind
@@ -60,23 +69,40 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// How long one try may sleep: short tries made waiting warps take issue slots from working ones.
-constexpr uint32_t kSleepNs = 1000000;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok) : "r"(bar), "r"(parity), "r"(kSleepNs) : "memory");
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for a phase; gives up (and tells the other roles) after about two seconds, so that no
-// mistake in the schedule can hang the device.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-    long long t0 = 0;
+// One arrival for the whole warp, after every lane's work before it: 128 arrivals of a warpgroup on
+// one barrier are served one after the other.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// Waits for a phase, all lanes of the warp together; gives up (and tells the other roles) after
+// about two seconds, so that no mistake in the schedule can hang the device. Both results are the
+// same in every lane. The first try stands alone: a phase that is over costs 60 clocks this way and
+// 190 with the limits in its loop, and the issuing warps wait six times per key tile.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+    if (__all_sync(kFull, mbar_try(bar, parity))) return true;
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (!__all_sync(kFull, mbar_try(bar, parity))) {
+        if (__any_sync(kFull, *stop != 0 || clock64() - t0 > 4000000000LL)) {
+            *stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a single lane.
+__device__ __forceinline__ bool lane_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+    const long long t0 = clock64();
     while (!mbar_try(bar, parity)) {
-        const long long t = clock64();
-        if (t0 == 0) t0 = t;
-        if (*stop != 0 || t - t0 > 4000000000LL) {
+        if (*stop != 0 || clock64() - t0 > 4000000000LL) {
             *stop = 1;
             return false;
         }
@@ -161,8 +187,8 @@ __device__ __forceinline__ uint32_t op_addr(int row, int chunk) {   // chunk of 
 // and groups of 8 tokens every 1024. Only the low word's address changes from one product to the next.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16); }
-// f32 accumulator, f16 operands, N = M = 128; bit 16: B is MN-major
-constexpr uint32_t kIdescQK = (1u << 4) | ((kKeys / 8) << 17) | ((kRows / 16) << 24);
+// f32 accumulator, f16 operands, M = 128, N = 64 (scores) or 128; bit 16: B is MN-major
+constexpr uint32_t kIdescQK = (1u << 4) | ((kHalf / 8) << 17) | ((kRows / 16) << 24);
 constexpr uint32_t kIdescPV = (1u << 4) | (1u << 16) | ((kD / 8) << 17) | ((kRows / 16) << 24);
 
 // One K = 16 step, A from shared memory or from TMEM; acc 0 overwrites D, 1 adds to it.
@@ -268,21 +294,23 @@ __device__ __forceinline__ bool chunk_next(const ChunkArgs& a, ChunkWalk& w, Chu
     return false;
 }
 
-// Raw packed subtiles (32 tokens of one kv head) on their way from memory: codes, scales and
-// zeros of keys and values, as bulk copies. As many stages as fit beside the operand tiles.
+// Raw packed tokens on their way from memory: a stage holds two subtiles (32 tokens
+// of one kv head each: codes, scales and zeros of keys and values). As many stages as fit
+// beside the operand tiles.
 template <int KB, int VB>
 struct RawLayout {
     static constexpr int kKc = 0, kKs = kTile * kD * KB / 8, kKz = kKs + kD * 2, kVc = kKz + kD * 2;
-    static constexpr int kVs = kVc + kTile * kD * VB / 8, kVz = kVs + 256, kBytes = kVz + 256;   // 128 of the last two used when G = 64
-    static constexpr int kStages = KB + VB == 4 ? 10 : KB + VB == 6 ? 8 : 6;
+    static constexpr int kVs = kVc + kTile * kD * VB / 8, kVz = kVs + 256, kSub = kVz + 256;   // 128 of the last two used when G = 64
+    static constexpr int kBytes = 2 * kSub;
+    static constexpr int kStages = KB + VB == 4 ? 5 : KB + VB == 6 ? 4 : 3;
 };
-constexpr int kRawMax = 10;
+constexpr int kRawMax = 5;
 constexpr int kSegs = 4;                  // segments announced ahead (warp 18 walks, every role follows)
-constexpr int kSegReaders = 18;           // warps 0 .. 17
+constexpr int kSegReaders = 19;           // every warp but the walking one
 
 struct ChunkShared {
     uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], s_full[4], p_full[4], o_step[4];   // all but the first: [softmax warpgroup][half]
     uint64_t raw_full[kRawMax], raw_empty[kRawMax], hand_full, hand_empty, seg_full[kSegs], seg_empty[kSegs];
     ChunkSeg seg[kSegs];
     float hand_m[kRows], hand_l[kRows];   // state of the second softmax warpgroup at the end of a narrow segment
@@ -374,9 +402,19 @@ __device__ __forceinline__ void fill_packed(const unsigned char* st, int gsh, in
     constexpr int BITS = VALUES ? VB : KB;
     constexpr int kRowBytes = kD * BITS / 8, kSpanBytes = 2 * BITS;
     const unsigned char* codes = st + (VALUES ? Raw::kVc : Raw::kKc) + row_lo * kRowBytes + span * kSpanBytes;
-    uint32_t sc[8], zr[8];
-    const unsigned char* meta = nullptr;
-    const int vsh = 8 - gsh;   // log2 of the bytes of a token's value scales, 2 D / G
+    // every load of the subtile before its first store (a store could alias a later load, so the
+    // compiler would keep them in order)
+    uint32_t w[4][BITS / 2], sc[8], zr[8], s1[4], z1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (BITS == 2) {
+            w[k][0] = *reinterpret_cast<const uint32_t*>(codes + 8 * k * kRowBytes);
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(codes + 8 * k * kRowBytes);
+            w[k][0] = x.x;
+            w[k][1] = x.y;
+        }
+    }
     if constexpr (!VALUES) {
         auto row = [&](int at, uint32_t (&out)[8]) {
             const uint4 a = *reinterpret_cast<const uint4*>(st + at + span * 32), b = *reinterpret_cast<const uint4*>(st + at + span * 32 + 16);
@@ -386,40 +424,28 @@ __device__ __forceinline__ void fill_packed(const unsigned char* st, int gsh, in
         row(Raw::kKs, sc);
         row(Raw::kKz, zr);
     } else {
-        meta = st + Raw::kVs + (row_lo << vsh) + (((span * 16) >> gsh) << 1);
-    }
-    // two rows at a time: the roles' loops together have to fit the instruction cache (all four
-    // rows unrolled, and the other loops likewise, ran at about half the speed)
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {
+        const int vsh = 8 - gsh;   // log2 of the bytes of a token's value scales, 2 D / G
+        const unsigned char* meta = st + Raw::kVs + (row_lo << vsh) + (((span * 16) >> gsh) << 1);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w[BITS / 2], c[8];
-            const unsigned char* code = codes + 8 * k * kRowBytes;
-            if constexpr (BITS == 2) {
-                w[0] = *reinterpret_cast<const uint32_t*>(code);
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2*>(code);
-                w[0] = x.x;
-                w[1] = x.y;
-            }
-            pair_codes<BITS>(w, c);
-            if constexpr (VALUES) {
-                const uint32_t s1 = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh));
-                const uint32_t z1 = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh) + (Raw::kVz - Raw::kVs));
-                const uint32_t s2 = prmt(s1, s1, 0x1010u), z2 = prmt(z1, z1, 0x1010u);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], s2, z2);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], sc[i], zr[i]);
-            }
-            *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(c[0], c[1], c[2], c[3]);
-            *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(c[4], c[5], c[6], c[7]);
+        for (int k = 0; k < 4; ++k) {
+            s1[k] = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh));
+            z1[k] = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh) + (Raw::kVz - Raw::kVs));
         }
-        codes += 16 * kRowBytes;
-        dst += 2048;
-        if constexpr (VALUES) meta += 16 << vsh;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t c[8];
+        pair_codes<BITS>(w[k], c);
+        if constexpr (VALUES) {
+            const uint32_t s2 = prmt(s1[k], s1[k], 0x1010u), z2 = prmt(z1[k], z1[k], 0x1010u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], s2, z2);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], sc[i], zr[i]);
+        }
+        *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(c[0], c[1], c[2], c[3]);
+        *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(c[4], c[5], c[6], c[7]);
     }
 }
 
@@ -495,27 +521,30 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
 
     if (tid == 0) {
         for (int i = 0; i < kKvStages; ++i) {
-            mbar_init(smem_u32(&sh.k_full[i]), 128);
-            mbar_init(smem_u32(&sh.k_empty[i]), 1);
-            mbar_init(smem_u32(&sh.v_full[i]), 128);
-            mbar_init(smem_u32(&sh.v_empty[i]), 1);
+            mbar_init(smem_u32(&sh.k_full[i]), 4);
+            mbar_init(smem_u32(&sh.k_empty[i]), 2);   // one per issuing warp
+            mbar_init(smem_u32(&sh.v_full[i]), 4);
+            mbar_init(smem_u32(&sh.v_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.q_full[i]), 128);
-            mbar_init(smem_u32(&sh.s_full[i]), 1);
-            mbar_init(smem_u32(&sh.p_full[i]), 128);
-            mbar_init(smem_u32(&sh.o_done[i]), 1);
+            mbar_init(smem_u32(&sh.q_full[i]), 4);
+            mbar_init(smem_u32(&sh.s_full[2 * i]), 1);
+            mbar_init(smem_u32(&sh.s_full[2 * i + 1]), 1);
+            mbar_init(smem_u32(&sh.p_full[2 * i]), 4);
+            mbar_init(smem_u32(&sh.p_full[2 * i + 1]), 4);
+            mbar_init(smem_u32(&sh.o_step[2 * i]), 1);
+            mbar_init(smem_u32(&sh.o_step[2 * i + 1]), 1);
         }
         for (int i = 0; i < Raw::kStages; ++i) {
-            mbar_init(smem_u32(&sh.raw_full[i]), 1);
+            mbar_init(smem_u32(&sh.raw_full[i]), 32);   // the loader's lanes
             mbar_init(smem_u32(&sh.raw_empty[i]), 4);   // the warps that read a subtile
         }
         for (int i = 0; i < kSegs; ++i) {
             mbar_init(smem_u32(&sh.seg_full[i]), 1);
             mbar_init(smem_u32(&sh.seg_empty[i]), kSegReaders);
         }
-        mbar_init(smem_u32(&sh.hand_full), 128);
-        mbar_init(smem_u32(&sh.hand_empty), 128);
+        mbar_init(smem_u32(&sh.hand_full), 4);
+        mbar_init(smem_u32(&sh.hand_empty), 4);
         sh.stop = 0;
         sh.idx = INT64_MAX;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -574,12 +603,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     bool ok = true;
     // segment i of this CTA in sh.seg: whether there is one, and the word that this warp is done with it
     auto seg_next = [&](uint32_t i) {
-        ok = mbar_wait(smem_u32(&sh.seg_full[i % kSegs]), (i / kSegs) & 1, stop);
+        ok = warp_wait(smem_u32(&sh.seg_full[i % kSegs]), (i / kSegs) & 1, stop);
         return ok && sh.seg[i % kSegs].x1 > 0;
     };
     auto seg_done = [&](uint32_t i) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.seg_empty[i % kSegs]));
+        warp_arrive(smem_u32(&sh.seg_empty[i % kSegs]));
     };
 
     if (warp < kChunkSoftmaxWarps) {
@@ -590,8 +618,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
         const int wg = warp >> 2, r = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>(warp & 3) << 21;     // this warp's 32 TMEM lanes
         const uint32_t t_s = tmem + lane_off + wg * kKeys, t_o = tmem + lane_off + 2 * kKeys + wg * kD;
-        uint32_t ns = 0, nq = 0, nh = 0;    // score tiles, segments and handed states so far
-        for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+        uint32_t ns = 0, nh = 0;    // key tiles and handed states so far
+        for (uint32_t si = 0; ok && seg_next(si); seg_done(si), ++si) {
             const ChunkSeg& s = sh.seg[si % kSegs];
             const bool narrow = s.it.rows <= kRows;
             const int tile = narrow ? 0 : wg, step = narrow ? 2 : 1;
@@ -634,7 +662,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                         store_rows(qt, r, sp, o);
                     }
                     proxy_fence();
-                    mbar_arrive(smem_u32(&sh.q_full[tile]));
+                    warp_arrive(smem_u32(&sh.q_full[tile]));
                 }
             }
             // tokens this row sees: [lo, pos] and [0, sinks)
@@ -644,108 +672,126 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             const int tile_first = len + (s.it.row0 + tile * kRows) / g;   // position of the row tile's first query
             const int tile_last = len + (s.it.row0 + tile * kRows + kRows - 1) / g;
 
-            float m = -CUDART_INF_F, l = 0.0f;
+            float m = -CUDART_INF_F;         // reference maximum, log2 units
+            float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};   // parts of the row's sum
             const int j0 = s.x0 + (narrow ? wg : 0);
             for (int j = j0; j < s.x1; j += step) {
-                ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.s_full[wg]), ns & 1, stop));
-                if (!ok) break;
-                ++ns;
-                if (!warp_live) {     // no row to serve: its products go nowhere
-                    mbar_arrive(smem_u32(&sh.p_full[wg]));
-                    continue;
-                }
-                tc_fence_after();
                 const int t0 = (j < s.it.st ? j : j + s.it.skip) * kKeys;
                 const bool cut = t0 + kKeys - 1 > tile_first ||
                                  (a.window > 0 && t0 <= tile_last - a.window && t0 + kKeys > snk);
                 // the row's bounds inside this tile: columns [c_lo, c_hi) and [0, c_snk)
                 const int c_hi = pos + 1 - t0, c_lo = lo - t0, c_snk = snk - t0;
-                // Both passes go by 64 columns in loops that are not unrolled: the roles of this kernel run different
-                // code at the same time, and with everything unrolled they waited for instructions.
-                auto mask = [&](float (&y)[2][32], int c0) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (c0 + i >= c_hi || (c0 + i < c_lo && c0 + i >= c_snk)) y[i >> 5][i & 31] = -CUDART_INF_F;
-                };
-                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll 1
-                for (int q = 0; q < kKeys; q += 64) {
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t t_sb = t_s + b * kHalf, p_bar = smem_u32(&sh.p_full[2 * wg + b]);
+                    ok = warp_wait(smem_u32(&sh.s_full[2 * wg + b]), ns & 1, stop);
+                    if (!ok) break;
+                    if (!warp_live) {     // no row to serve: its products go nowhere
+                        warp_arrive(p_bar);
+                        continue;
+                    }
+                    tc_fence_after();
+                    // By 32 columns: their maximum, then their exponentials against the reference. Only where the
+                    // maximum has outrun the reference by more than the lag does the reference move up, and what is
+                    // there in its units (the sum, this row's output, the first columns' probabilities) is scaled
+                    // down. (Rolled by halves: the roles of this kernel run different code at the same time and
+                    // share the instruction cache.)
                     float x[2][32];
-                    tc_ld32(x[0], t_s + q);
-                    tc_ld32(x[1], t_s + q + 32);
+                    tc_ld32(x[0], t_sb);
+                    tc_ld32(x[1], t_sb + 32);
                     tc_wait_ld();
-                    if (__builtin_expect(cut, 0)) mask(x, q);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx[i & 1] = fmaxf(mx[i & 1], fmaxf(x[i >> 4][2 * (i & 15)], x[i >> 4][2 * (i & 15) + 1]));
-                }
-                const float top = fmaxf(mx[0], mx[1]) * sl;
-                const bool grow = m == -CUDART_INF_F ? top > m : top > m + kLag;
-                if (__any_sync(kFull, grow)) {
-                    const float alpha = grow ? exp2_ftz(m - top) : 1.0f;     // 0 while m is -inf
-                    l *= alpha;
-                    if (grow) m = top;
-                    if (j > j0) {     // the products of the tiles before are complete (they precede these scores)
-#pragma unroll 1
-                        for (int q = 0; q < kD / 32; ++q) {
-                            float y[32];
-                            tc_ld32(y, t_o + 32 * q);
-                            tc_wait_ld();
+                    for (int q = 0; q < 2; ++q) {
+                        float(&y)[32] = x[q];
+                        if (__builtin_expect(cut, 0)) {
+                            const int c1 = kHalf * b + 32 * q;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) y[i] *= alpha;
-                            tc_st32(t_o + 32 * q, y);
+                            for (int i = 0; i < 32; ++i)
+                                if (c1 + i >= c_hi || (c1 + i < c_lo && c1 + i >= c_snk)) y[i] = -CUDART_INF_F;
                         }
-                        tc_wait_st();
-                    }
-                }
-                const float mref = m == -CUDART_INF_F ? 0.0f : m;
-                const float2 sl2 = make_float2(sl, sl), mn2 = make_float2(-mref, -mref);
-                float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll 1
-                for (int q = 0; q < kKeys; q += 64) {
-                    float x[2][32];
-                    tc_ld32(x[0], t_s + q);
-                    tc_ld32(x[1], t_s + q + 32);
-                    tc_wait_ld();
-                    if (__builtin_expect(cut, 0)) mask(x, q);
-                    float p[32];
+                        float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float2 e = fma2(make_float2(x[i >> 4][2 * (i & 15)], x[i >> 4][2 * (i & 15) + 1]), sl2, mn2);
-                        e.x = exp2_ftz(e.x);
-                        e.y = exp2_ftz(e.y);
-                        acc[i & 1] = add2(acc[i & 1], e);
-                        p[i] = __uint_as_float(pack_h2(e.x, e.y));
+                        for (int i = 0; i < 16; ++i) mx[i & 1] = fmaxf(mx[i & 1], fmaxf(y[2 * i], y[2 * i + 1]));
+                        const float top = fmaxf(mx[0], mx[1]) * sl;
+                        const bool grow = m == -CUDART_INF_F ? top > m : top > m + kLag;
+                        if (__builtin_expect(__any_sync(kFull, grow), 0)) {
+                            const float alpha = grow ? exp2_ftz(m - top) : 1.0f;     // 0 while m is -inf
+                            if (grow) m = top;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                l[i].x *= alpha;
+                                l[i].y *= alpha;
+                            }
+                            if (q == 1) {
+                                const uint32_t alpha2 = pack_h2(alpha, alpha);
+                                float u[16];
+                                uint32_t v[16];
+                                tc_wait_st();
+                                tc_ld16(u, t_sb);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = hmul2(__float_as_uint(u[i]), alpha2);
+                                tc_st16(t_sb, v);
+                            }
+                            if (j > j0 || b > 0) {     // once the products of the halves before are complete
+                                ok = warp_wait(smem_u32(&sh.o_step[2 * wg + (b ^ 1)]), (ns + b - 1) & 1, stop);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < kD / 16; ++c) {
+                                    float u[16];
+                                    uint32_t v[16];
+                                    tc_ld16(u, t_o + 16 * c);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(u[i] * alpha);
+                                    tc_st16(t_o + 16 * c, v);
+                                }
+                            }
+                        }
+                        const float mref = m == -CUDART_INF_F ? 0.0f : m;
+                        const float2 sl2 = make_float2(sl, sl), mn2 = make_float2(-mref, -mref);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 e = fma2(make_float2(y[2 * i], y[2 * i + 1]), sl2, mn2);
+                            e.x = exp2_ftz(e.x);
+                            e.y = exp2_ftz(e.y);
+                            l[i & 1] = add2(l[i & 1], e);
+                            p[i] = pack_h2(e.x, e.y);
+                        }
+                        tc_st16(t_sb + 16 * q, p);   // over scores that have been read
                     }
-                    tc_st32(t_s + (q >> 1), p);   // over scores that have been read
+                    if (!ok) break;
+                    tc_wait_st();
+                    tc_fence_before();
+                    warp_arrive(p_bar);
                 }
-                acc[0] = add2(acc[0], acc[1]);
-                l += acc[0].x + acc[0].y;
-                tc_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_u32(&sh.p_full[wg]));
+                if (!ok) break;
+                ++ns;
             }
             const bool any = j0 < s.x1;      // this warpgroup had tiles
             if (any) {
-                ok = ok && __all_sync(kFull, mbar_wait(smem_u32(&sh.o_done[wg]), nq & 1, stop));
+                ok = ok && warp_wait(smem_u32(&sh.o_step[2 * wg + 1]), (ns - 1) & 1, stop);
                 if (!ok) break;
-                ++nq;
                 tc_fence_after();
             }
+            float sum = (l[0].x + l[0].y) + (l[1].x + l[1].y);
             float f0 = 1.0f, f1 = 0.0f;      // factors of the two states of a narrow segment
             bool both = false;
             if (narrow && s.x1 - s.x0 > 1) {
                 if (wg == 1) {
                     // hand the state over; the output columns are read from TMEM by the other warpgroup
                     sh.hand_m[r] = m;
-                    sh.hand_l[r] = l;
+                    sh.hand_l[r] = sum;
                     tc_fence_before();
-                    mbar_arrive(smem_u32(&sh.hand_full));
-                    ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.hand_empty), nh & 1, stop));
+                    warp_arrive(smem_u32(&sh.hand_full));
+                    ok = warp_wait(smem_u32(&sh.hand_empty), nh & 1, stop);
                     ++nh;
                     tc_fence_after();
                     continue;
                 }
-                ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.hand_full), nh & 1, stop));
+                ok = warp_wait(smem_u32(&sh.hand_full), nh & 1, stop);
                 if (!ok) break;
                 ++nh;
                 tc_fence_after();
@@ -755,14 +801,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                     f0 = exp2_ftz(m - mt);
                     f1 = exp2_ftz(m1 - mt);
                 }
-                l = l * f0 + l1 * f1;
+                sum = sum * f0 + l1 * f1;
                 m = mt;
             } else if (narrow && wg == 1) {
                 continue;
             }
             const bool whole = s.x0 == 0 && s.x1 == s.it.nt;
             if (whole) {
-                const float inv = 1.0f / l;
+                const float inv = 1.0f / sum;
                 f0 *= inv;
                 f1 *= inv;
             }
@@ -797,11 +843,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             }
             if (both) {
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh.hand_empty));
+                warp_arrive(smem_u32(&sh.hand_empty));
             }
             if (!whole && live) {
                 rec[kRows * kD + r] = m;
-                rec[kRows * kD + kRows + r] = l;
+                rec[kRows * kD + kRows + r] = sum;
             }
             if (!whole && s.x0 == 0 && tid == 0) {
                 ChunkInfo f;
@@ -820,16 +866,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
         auto operands = [&](auto values) {
             constexpr bool VALUES = decltype(values)::value;
             constexpr int BITS = VALUES ? VB : KB;
-            // warps 0 and 1 of the group take the even subtiles of a tile, 2 and 3 the odd ones; each warp has
+            // warps 0 and 1 of the group take the first two subtiles of a tile, 2 and 3 the others; each warp has
             // half of the spans
-            const int odd = (warp >> 1) & 1, row_lo = lane & 7, span = (lane >> 3) + 4 * (warp & 1);
+            const int half = (warp >> 1) & 1, row_lo = lane & 7, span = (lane >> 3) + 4 * (warp & 1);
             const uint32_t a0 = op_addr(row_lo, 2 * span), a1 = op_addr(row_lo, 2 * span + 1);
             const int gsh = a.G == 64 ? 6 : 5;
             uint64_t* full = VALUES ? sh.v_full : sh.k_full;
             uint64_t* empty = VALUES ? sh.v_empty : sh.k_empty;
             unsigned char* tiles = VALUES ? sv_tile : sk_tile;
-            uint32_t n = 0, raw0 = 0, raw_par = 0;    // tiles so far; stage and parity of the tile's first raw subtile
-            for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+            uint32_t n = 0, raw0 = 0, raw_par = 0;    // tiles so far; the tile's first raw stage and its parity
+            for (uint32_t si = 0; ok && seg_next(si); seg_done(si), ++si) {
                 const ChunkSeg& s = sh.seg[si % kSegs];
                 const kivi_seq& sq = a.seqs[s.it.b];
                 const int np = static_cast<int>(n_packed(s.it.L, a.R, a.G));
@@ -846,9 +892,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                     const int t0 = (j < lst ? j : j + skip) * kKeys;
                     const int packed = np <= t0 ? 0 : np - t0 >= kKeys ? kKeys / kTile : (np - t0) / kTile;   // subtiles
                     auto wait_empty = [&]() {
-                        if (use > 0) ok = __all_sync(kFull, mbar_wait(smem_u32(&empty[st]), (use - 1) & 1, stop));
+                        if (use > 0) ok = warp_wait(smem_u32(&empty[st]), (use - 1) & 1, stop);
                     };
-                    unsigned char* dst = tiles + st * kOpBytes + odd * (kTile * 128);
+                    unsigned char* dst = tiles + st * kOpBytes + half * (2 * kTile * 128);
                     auto stored = [&](const uint32_t (&x)[4][8], unsigned char* to) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -858,126 +904,139 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                             *reinterpret_cast<uint4*>(to + a1 + 1024 * k) = make_uint4(o[4], o[5], o[6], o[7]);
                         }
                     };
-                    if (odd < packed) {
+                    if (2 * half < packed) {
+                        const bool wrap = raw0 + half >= Raw::kStages;
+                        const uint32_t slot = wrap ? raw0 + half - Raw::kStages : raw0 + half;
+                        ok = warp_wait(smem_u32(&sh.raw_full[slot]), raw_par ^ wrap, stop);
+                        if (!ok) break;
                         wait_empty();
                         if (!ok) break;
+                        const unsigned char* from = raw_ring + slot * Raw::kBytes;
+                        const int subs = packed - 2 * half < 2 ? 1 : 2;
 #pragma unroll 1
-                        for (int sub = odd; sub < packed; sub += 2, dst += 2 * kTile * 128) {
-                            const bool wrap = raw0 + sub >= Raw::kStages;
-                            const uint32_t slot = wrap ? raw0 + sub - Raw::kStages : raw0 + sub;
-                            ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.raw_full[slot]), raw_par ^ wrap, stop));
-                            if (!ok) break;
-                            fill_packed<KB, VB, VALUES>(raw_ring + slot * Raw::kBytes, gsh, row_lo, span, dst, a0, a1);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[slot]));
+                        for (int i = 0; i < subs; ++i) {
+                            fill_packed<KB, VB, VALUES>(from, gsh, row_lo, span, dst, a0, a1);
+                            from += Raw::kSub;
+                            dst += kTile * 128;
                         }
-                        if (!ok) break;
-                        if (odd + 2 >= packed) {     // the tile's second half is stored tokens
+                        warp_arrive(smem_u32(&sh.raw_empty[slot]));
+                        if (subs < 2) {     // the second subtile is stored tokens
                             uint32_t x[4][8];
-                            load_stored(src, t0 + (odd + 2) * kTile, row_lo, span, x);
+                            load_stored(src, t0 + (2 * half + 1) * kTile, row_lo, span, x);
                             stored(x, dst);
                         }
                     } else {
                         uint32_t x[4][8];
-                        load_stored(src, t0 + odd * kTile, row_lo, span, x);
+                        load_stored(src, t0 + 2 * half * kTile, row_lo, span, x);
                         wait_empty();
                         if (!ok) break;
                         stored(x, dst);
-                        load_stored(src, t0 + (odd + 2) * kTile, row_lo, span, x);
-                        stored(x, dst + 2 * kTile * 128);
+                        load_stored(src, t0 + (2 * half + 1) * kTile, row_lo, span, x);
+                        stored(x, dst + kTile * 128);
                     }
-                    raw0 += packed;
+                    raw0 += (packed + 1) / 2;
                     if (raw0 >= Raw::kStages) {
                         raw0 -= Raw::kStages;
                         raw_par ^= 1;
                     }
                     proxy_fence();
-                    mbar_arrive(smem_u32(&full[st]));
+                    warp_arrive(smem_u32(&full[st]));
                 }
             }
         };
         if (warp < 12) operands(std::integral_constant<bool, false>{});
         else operands(std::integral_constant<bool, true>{});
-    } else if (warp == 16) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        // ------------------------------------------------ tensor-core issue: the whole warp walks, one lane issues
-        uint32_t n = 0, np[2] = {0, 0}, nq[2] = {0, 0};   // key tiles, probability tiles, segments so far
-        const uint32_t kb0 = smem_u32(sk_tile), vb0 = smem_u32(sv_tile), qb0 = smem_u32(sq_tile);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = __all_sync(kFull, mbar_wait(smem_u32(bar), parity, stop));
-            return ok;
-        };
-        for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
-            // A segment is a row of events: event e is key tile j(e) for the softmax warpgroup t = e & 1. Wide: both
-            // warpgroups (row tiles) take every tile, e = 2 j + t; narrow: they take tiles in turn, e = j. Two
-            // score products run ahead; after the products of event e its S is free for the scores of e + 2. One
-            // rolled loop for both: the issuing code has to stay small to stay cached.
-            const int narrow = sh.seg[si % kSegs].it.rows <= kRows;
-            const int cnt = sh.seg[si % kSegs].x1 - sh.seg[si % kSegs].x0, events = narrow ? cnt : 2 * cnt;
-            const int wide = 1 - narrow;
-            if (!wait(&sh.q_full[0], nq[0]++ & 1)) break;
-            if (wide && !wait(&sh.q_full[1], nq[1]++ & 1)) break;
-#pragma unroll 1
-            for (int e = -2; e < events; ++e) {
-                const uint32_t t = e & 1;
-                if (e >= 0) {
-                    const uint32_t u = n + (e >> wide), st = u % kKvStages;
-                    if (!wait(&sh.v_full[st], (u / kKvStages) & 1)) break;
-                    if (!wait(&sh.p_full[t], (t ? np[1]++ : np[0]++) & 1)) break;
-                    tc_fence_after();
-                    // (broadcast, so that the compiler keeps the operands in uniform registers)
-                    const uint32_t v = __shfl_sync(kFull, desc_lo(vb0 + st * kOpBytes, kRows * 128), 0);
-                    const uint32_t d = __shfl_sync(kFull, tmem + 2 * kKeys + t * kD, 0), p = __shfl_sync(kFull, tmem + t * kKeys, 0);
-                    const uint32_t acc = __shfl_sync(kFull, e > 1 ? 1u : 0u, 0);
-                    if (elect_one()) {
-                        mma_ts(d, p, v, kIdescPV, acc);
-#pragma unroll
-                        for (uint32_t i = 1; i < kKeys / 16; ++i) mma_ts(d, p + 8 * i, v + i * (2048 >> 4), kIdescPV, 1);
-                        if (narrow || t) tc_commit(smem_u32(&sh.v_empty[st]));
-                        if (e + 2 >= events) tc_commit(smem_u32(&sh.o_done[t]));
-                    }
-                }
-                if (e + 2 < events) {
-                    const uint32_t u = n + ((e + 2) >> wide), st = u % kKvStages;
-                    if (!wait(&sh.k_full[st], (u / kKvStages) & 1)) break;
-                    tc_fence_after();
-                    const uint32_t q = __shfl_sync(kFull, desc_lo(qb0 + wide * t * kOpBytes, 16), 0);
-                    const uint32_t k = __shfl_sync(kFull, desc_lo(kb0 + st * kOpBytes, 16), 0), d = __shfl_sync(kFull, tmem + t * kKeys, 0);
-                    if (elect_one()) {
-#pragma unroll
-                        for (uint32_t i = 0; i < kD / 16; ++i) {
-                            const uint32_t off = (i >> 2) * ((kRows * 128) >> 4) + (i & 3) * 2;
-                            mma_ss(d, q + off, k + off, kIdescQK, i > 0);
-                        }
-                        tc_commit(smem_u32(&sh.s_full[t]));
-                        if (narrow || t) tc_commit(smem_u32(&sh.k_empty[st]));
-                    }
-                }
-                __syncwarp();
-            }
-            n += cnt;
-        }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-        if (warp == 17) {
-            // -------------------------------------------- raw packed subtiles: lane i < 6 copies buffer i
+        if (warp == 16 || warp == 19) {
+            // ------------------------------------------------ tensor-core issue: warp 16 for softmax warpgroup 0, 19 for 1.
+            // (The tensor core takes few products ahead, so a single issuing warp left it idle while it waited.) The
+            // whole warp walks, one lane issues.
+            const uint32_t t = warp == 16 ? 0 : 1;
+            uint32_t n = 0, np = 0, nq = 0;   // key tiles, probability tiles, segments so far
+            const uint32_t kb0 = smem_u32(sk_tile), vb0 = smem_u32(sv_tile), qb0 = smem_u32(sq_tile);
+            const uint32_t d_s = __shfl_sync(kFull, tmem + t * kKeys, 0), d_o = __shfl_sync(kFull, tmem + 2 * kKeys + t * kD, 0);
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = warp_wait(smem_u32(bar), parity, stop);
+                return ok;
+            };
+            for (uint32_t si = 0; ok && seg_next(si); seg_done(si), ++si) {
+                // Wide segments: this warpgroup (its row tile) takes every key tile; narrow ones: the warpgroups take
+                // them in turn, and the one that takes a tile gives its stage back for both. Scores run one tile ahead:
+                // S is free for the next scores after the products of the tile before.
+                const ChunkSeg& s = sh.seg[si % kSegs];
+                const uint32_t narrow = s.it.rows <= kRows, cnt = s.x1 - s.x0, step = 1 + narrow;
+                // (both warps follow the first query tile's barrier: it completes once a segment, after
+                // everything of the segment before)
+                if (!wait(&sh.q_full[0], si & 1)) break;
+                if (!narrow && t != 0 && !wait(&sh.q_full[1], nq++ & 1)) break;
+                const uint32_t q = __shfl_sync(kFull, desc_lo(qb0 + (narrow ? 0 : t) * kOpBytes, 16), 0);
+                // halves of this warpgroup's tiles: half i is half i & 1 of its tile i >> 1, tile (i >> 1) step + narrow t
+                // of the segment; scores run two halves ahead
+                const uint32_t halves = 2 * ((cnt + narrow - narrow * t) / step);
+#pragma unroll 1
+                for (uint32_t i = 0; i < halves + 2; ++i) {
+                    const uint32_t b = i & 1;
+                    if (i >= 2) {          // products of half i - 2
+                        const uint32_t u = n + ((i - 2) >> 1) * step + narrow * t, st = u % kKvStages;
+                        if (!wait(&sh.v_full[st], (u / kKvStages) & 1) || !wait(&sh.p_full[2 * t + b], (np >> 1) & 1)) break;
+                        ++np;
+                        tc_fence_after();
+                        // (broadcast, so that the compiler keeps the operands in uniform registers)
+                        const uint32_t v = __shfl_sync(kFull, desc_lo(vb0 + st * kOpBytes + b * (kHalf * 128), kRows * 128), 0);
+                        const uint32_t p = __shfl_sync(kFull, d_s + b * kHalf, 0), acc = __shfl_sync(kFull, i > 2 ? 1u : 0u, 0);
+                        if (elect_one()) {
+                            mma_ts(d_o, p, v, kIdescPV, acc);
+#pragma unroll
+                            for (uint32_t k = 1; k < kHalf / 16; ++k) mma_ts(d_o, p + 8 * k, v + k * (2048 >> 4), kIdescPV, 1);
+                            tc_commit(smem_u32(&sh.o_step[2 * t + b]));
+                            if (b) {
+                                tc_commit(smem_u32(&sh.v_empty[st]));
+                                if (narrow) tc_commit(smem_u32(&sh.v_empty[st]));
+                            }
+                        }
+                    }
+                    if (i < halves) {      // scores of half i
+                        const uint32_t u = n + (i >> 1) * step + narrow * t, st = u % kKvStages;
+                        if (!wait(&sh.k_full[st], (u / kKvStages) & 1)) break;
+                        tc_fence_after();
+                        const uint32_t k = __shfl_sync(kFull, desc_lo(kb0 + st * kOpBytes + b * (kHalf * 128), 16), 0);
+                        const uint32_t d = __shfl_sync(kFull, d_s + b * kHalf, 0);
+                        if (elect_one()) {
+#pragma unroll
+                            for (uint32_t c = 0; c < kD / 16; ++c) {
+                                const uint32_t off = (c >> 2) * ((kRows * 128) >> 4) + (c & 3) * 2;
+                                mma_ss(d, q + off, k + off, kIdescQK, c > 0);
+                            }
+                            tc_commit(smem_u32(&sh.s_full[2 * t + b]));
+                            if (b) {
+                                tc_commit(smem_u32(&sh.k_empty[st]));
+                                if (narrow) tc_commit(smem_u32(&sh.k_empty[st]));
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                n += cnt;
+            }
+        } else if (warp == 17) {
+            // -------------------------------------------- raw packed tokens, 16 bytes a lane and copy. (Bulk copies of
+            // the six buffers' runs, 256 to 1024 bytes each, made the kernel 3 % slower where memory counts: 64 x 32768
+            // tokens, 4 new ones each.)
             uint32_t slot = 0, par = 0;
             bool full_turn = false;
-            // Buffer of this lane: its bytes per subtile, its place in a raw stage, and the strides of a group
-            // and of a subtile within it.
-            const int nv = kD / a.G, tpg = a.G / kTile, bits = lane == 0 ? KB : VB;
-            const bool codes = lane == 0 || lane == 3, vmeta = lane > 3;
-            const uint32_t len = codes ? kTile * kD * bits / 8 : vmeta ? kTile * nv * 2 : kD * 2;
-            const uint32_t sub_stride = codes || vmeta ? len : 0, group_stride = sub_stride != 0 ? sub_stride * tpg : kD * 2;
-            const uint32_t at = lane == 0 ? Raw::kKc : lane == 1 ? Raw::kKs : lane == 2 ? Raw::kKz
-                              : lane == 3 ? Raw::kVc : lane == 4 ? Raw::kVs : Raw::kVz;
-            const uint32_t bytes = kTile * kD * (KB + VB) / 8 + 2 * kD * 2 + 2 * kTile * nv * 2;
-            for (uint32_t si = 0; ok && __all_sync(kFull, seg_next(si)); seg_done(si), ++si) {
+            constexpr uint32_t kKcb = kTile * kD * KB / 8, kVcb = kTile * kD * VB / 8;    // codes of a subtile
+            const int tpg = a.G / kTile;
+            const uint32_t vmeta = kTile * (kD / a.G) * 2, vlanes = vmeta / 16;           // value scales (or zeros) of a subtile
+            for (uint32_t si = 0; ok && seg_next(si); seg_done(si), ++si) {
                 const ChunkSeg& s = sh.seg[si % kSegs];
                 const kivi_seq& sq = a.seqs[s.it.b];
-                const unsigned char* base = static_cast<const unsigned char*>(
-                    lane == 0 ? static_cast<const void*>(sq.k_codes) : lane == 1 ? sq.k_scale : lane == 2 ? sq.k_zero
-                    : lane == 3 ? static_cast<const void*>(sq.v_codes) : lane == 4 ? sq.v_scale : sq.v_zero);
+                // this lane's place in each buffer: codes at 16 lane, scales and zeros by half warps
+                const unsigned char* kc = sq.k_codes + 16 * lane;
+                const unsigned char* vc = sq.v_codes + 16 * lane;
+                const unsigned char* km = reinterpret_cast<const unsigned char*>(lane < 16 ? sq.k_scale : sq.k_zero) + 16 * (lane & 15);
+                const unsigned char* vm = reinterpret_cast<const unsigned char*>((lane & vlanes) == 0 ? sq.v_scale : sq.v_zero) +
+                                          16 * (lane & (vlanes - 1));
                 const bool paged = seq_paged(sq);
                 const int32_t* table = sq.block_table;
                 const int h = s.h, x1 = s.x1, st = s.it.st, skip = s.it.skip;
@@ -987,27 +1046,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                 int page0 = -64, pages = 0;
                 for (int j = s.x0; ok && j < x1; ++j) {
                     const int t0 = (j < st ? j : j + skip) * (kKeys / kTile);
-                    for (int t = t0; t < t0 + kKeys / kTile && t < tiles; ++t) {
-                        const int group = tpg == 1 ? t : t >> 1;
-                        int64_t at_group = head + group;
-                        if (paged) {
-                            if (group < page0 || group >= page0 + 32) {
-                                page0 = group;
-                                pages = (page0 + lane) * tpg < tiles ? __ldg(table + page0 + lane) : 0;
-                            }
-                            at_group = static_cast<int64_t>(__shfl_sync(kFull, pages, group - page0)) * a.H + h;
-                        }
-                        if (full_turn) ok = __all_sync(kFull, mbar_wait(smem_u32(&sh.raw_empty[slot]), par ^ 1, stop));
+                    for (int t = t0; t < t0 + kKeys / kTile && t < tiles; t += 2) {
+                        if (full_turn) ok = warp_wait(smem_u32(&sh.raw_empty[slot]), par ^ 1, stop);
                         if (!ok) break;
-                        const uint32_t bar = smem_u32(&sh.raw_full[slot]);
-                        if (lane == 0)
-                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-                        __syncwarp();
-                        if (lane < 6)
-                            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                                         ::"r"(smem_u32(raw_ring + slot * Raw::kBytes) + at),
-                                         "l"(base + at_group * group_stride + (tpg == 1 ? 0 : t & 1) * sub_stride), "r"(len), "r"(bar)
-                                         : "memory");
+                        unsigned char* dst = raw_ring + slot * Raw::kBytes;
+                        const int subs = tiles - t < 2 ? 1 : 2;
+#pragma unroll 1
+                        for (int i = 0; i < subs; ++i, dst += Raw::kSub) {
+                            const int group = tpg == 1 ? t + i : t >> 1;
+                            int64_t at = head + group;                // the group's record
+                            if (paged) {
+                                if (group < page0 || group >= page0 + 32) {
+                                    page0 = group;
+                                    pages = (page0 + lane) * tpg < tiles ? __ldg(table + page0 + lane) : 0;
+                                }
+                                at = static_cast<int64_t>(__shfl_sync(kFull, pages, group - page0)) * a.H + h;
+                            }
+                            const int64_t rt = at * tpg + (tpg == 1 ? 0 : (t + i) & 1);   // the subtile's
+#pragma unroll
+                            for (uint32_t k = 0; k < kKcb; k += 512) cp_async16(dst + Raw::kKc + k + 16 * lane, kc + rt * kKcb + k);
+                            cp_async16(dst + (lane < 16 ? Raw::kKs : Raw::kKz) + 16 * (lane & 15), km + at * (kD * 2));
+#pragma unroll
+                            for (uint32_t k = 0; k < kVcb; k += 512) cp_async16(dst + Raw::kVc + k + 16 * lane, vc + rt * kVcb + k);
+                            if (lane < 2 * vlanes)
+                                cp_async16(dst + ((lane & vlanes) == 0 ? Raw::kVs : Raw::kVz) + 16 * (lane & (vlanes - 1)), vm + rt * vmeta);
+                        }
+                        // this lane's arrival, once its copies have landed
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.raw_full[slot])) : "memory");
                         if (++slot == Raw::kStages) {
                             slot = 0;
                             par ^= 1;
@@ -1016,15 +1081,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                     }
                 }
             }
-            // copies in flight land before the CTA ends (they have all been waited for, unless a wait ran out)
-            if (*stop != 0) {
-                const long long t1 = clock64();
-                for (uint32_t i = 0; i < Raw::kStages; ++i) {
-                    const uint32_t q = i < slot ? par : par ^ 1;    // parity of this stage's last use
-                    if (i >= slot && !full_turn) continue;
-                    while (!mbar_try(smem_u32(&sh.raw_full[i]), q) && clock64() - t1 < 4000000000LL) {}
-                }
-            }
+            asm volatile("cp.async.wait_all;" ::: "memory");   // nothing in flight when the CTA ends
         } else if (warp == 18 && lane == 0) {
             // -------------------------------------------- the walk over this CTA's share; x1 = 0 ends it
             ChunkWalk w;
@@ -1034,7 +1091,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                 ChunkSeg s;
                 more = chunk_next(a, w, s);
                 if (!more) s.x0 = s.x1 = 0;
-                if (i >= kSegs && !mbar_wait(smem_u32(&sh.seg_empty[i % kSegs]), (i / kSegs - 1) & 1, stop)) break;
+                if (i >= kSegs && !lane_wait(smem_u32(&sh.seg_empty[i % kSegs]), (i / kSegs - 1) & 1, stop)) break;
                 sh.seg[i % kSegs] = s;
                 mbar_arrive(smem_u32(&sh.seg_full[i % kSegs]));
             }
@@ -1043,17 +1100,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*stop != 0) {
+        // a wait ran out: let the products in flight finish (with a limit) before the TMEM goes
+        if (tid == 0) set_status(a.status, KIVI_ERR_CUDA);
+        if ((warp == 16 || warp == 19) && lane == 0) {
+            const uint32_t bar = smem_u32(&sh.warp_sum[warp]);
+            mbar_init(bar, 1);
+            tc_commit(bar);
+            const long long t0 = clock64();
+            while (!mbar_try(bar, 0) && clock64() - t0 < 4000000000LL) {}
+        }
+        __syncthreads();
+    }
     if (warp == 16) {
         tc_fence_after();
-        if (*stop != 0 && lane == 0) {
-            // a wait ran out: let the products in flight finish (with a limit) before the TMEM goes
-            set_status(a.status, KIVI_ERR_CUDA);
-            mbar_init(smem_u32(&sh.warp_sum[0]), 1);
-            tc_commit(smem_u32(&sh.warp_sum[0]));
-            const long long t0 = clock64();
-            while (!mbar_try(smem_u32(&sh.warp_sum[0]), 0) && clock64() - t0 < 4000000000LL) {}
-        }
-        __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
