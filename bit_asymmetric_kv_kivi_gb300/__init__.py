@@ -13,6 +13,7 @@ sizes and argument validation work on any host; compute calls raise
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -138,9 +139,11 @@ def _require_cuda(t: torch.Tensor, name: str) -> None:
 
 
 def _require(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torch.device) -> None:
-    """A contiguous tensor of this shape and type on this device (a device without an index is any)."""
-    _require_cuda(t, name)
-    if tuple(t.shape) != tuple(shape):
+    """A contiguous, 16-byte aligned tensor of this shape and type on this device (a device without
+    an index is any)."""
+    if not t.is_cuda or not t.is_contiguous():
+        _require_cuda(t, name)
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -148,6 +151,14 @@ def _require(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torc
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.data_ptr() % 16:
         raise ValueError(f"{name} must be 16-byte aligned")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Makes the tensors' device the current one, where it is not."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
@@ -216,6 +227,13 @@ class Config:
 
     def decode_weights_scratch_bytes(self, nseq: int, max_kv_len: int) -> int:
         return int(lib().kivi_decode_weights_scratch_bytes(self.c(), nseq, max_kv_len))
+
+    def chunk_scratch_bytes(self, nseq: int, max_new: int) -> int:
+        return int(lib().kivi_chunk_scratch_bytes(self.c(), nseq, max_new))
+
+
+def _evict_scratch_bytes(nseq: int, groups: int) -> int:
+    return int(lib().kivi_evict_scratch_bytes(nseq, groups))
 
 
 # ---------------------------------------------------------------- codec
@@ -331,6 +349,8 @@ class KVCache:
         self._ws = None
         self._scratch = None
         self._old = []
+        self._sizes = {}
+        self._c = self.cfg.c()
         rec = np.zeros((nseq, SEQ_STRUCT_BYTES // 8), dtype=np.uint64)
         for b in range(nseq):
             for i, name in enumerate(SEQ_FIELDS):
@@ -431,6 +451,13 @@ class KVCache:
             self._old.append(old)
         return make(max(need, 256), dtype=torch.uint8, device=self.device)
 
+    def _bytes(self, what, *key) -> int:
+        """A size that depends on the call's shape alone, asked of the library once."""
+        n = self._sizes.get((what, key))
+        if n is None:
+            n = self._sizes[what, key] = int(what(*key))
+        return n
+
     def _zeroed(self, need: int) -> torch.Tensor:
         """The workspace that every attention call leaves zero-filled, at least `need` bytes."""
         self._ws = self._grown(self._ws, need, torch.zeros)
@@ -458,9 +485,9 @@ class KVCache:
         tokens). q [nseq][Hq][D] (cfg dtype) -> out [nseq][Hq][D] fp32."""
         out, scale, mkl = self._decode_args(q, out, softmax_scale, max_kv_len)
         cfg = self.cfg
-        with torch.cuda.device(q.device):
-            ws = self._zeroed(cfg.decode_ext_workspace_bytes(self.nseq, mkl))
-            _check(lib().kivi_decode_window_attn(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
+        with _on(q.device):
+            ws = self._zeroed(self._bytes(cfg.decode_ext_workspace_bytes, self.nseq, mkl))
+            _check(lib().kivi_decode_window_attn(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
                                                  _ptr(out), scale, int(window), int(sinks), mkl, _ptr(ws), ws.numel(),
                                                  _ptr(self.status), _stream(q.device)), "kivi_decode_window_attn")
         return out
@@ -486,10 +513,10 @@ class KVCache:
         _require(weights_out, "weights_out", (self.nseq, stride), torch.float32, self.device)
         if weights_in is not None:
             _require(weights_in, "weights_in", (self.nseq, stride), torch.float32, self.device)
-        with torch.cuda.device(q.device):
-            ws = self._zeroed(cfg.decode_ext_workspace_bytes(self.nseq, mkl))
-            sc = self._any(cfg.decode_weights_scratch_bytes(self.nseq, mkl))
-            _check(lib().kivi_decode_attn_weights(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
+        with _on(q.device):
+            ws = self._zeroed(self._bytes(cfg.decode_ext_workspace_bytes, self.nseq, mkl))
+            sc = self._any(self._bytes(cfg.decode_weights_scratch_bytes, self.nseq, mkl))
+            _check(lib().kivi_decode_attn_weights(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
                                                   _ptr(out), _ptr(weights_in), _ptr(weights_out), stride, float(decay),
                                                   scale, mkl, _ptr(ws), ws.numel(), _ptr(sc), sc.numel(),
                                                   _ptr(self.status), _stream(q.device)), "kivi_decode_attn_weights")
@@ -514,9 +541,9 @@ class KVCache:
             _require(out, "out", q.shape, cfg.torch_dtype, q.device)
         scale = 1.0 / cfg.head_dim ** 0.5 if softmax_scale is None else softmax_scale
         mkl = int(self.max_len if max_kv_len is None else max_kv_len)
-        with torch.cuda.device(q.device):
-            sc = self._any(int(lib().kivi_chunk_scratch_bytes(cfg.c(), self.nseq, int(max_new))))
-            _check(lib().kivi_chunk_attn(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(k_ptrs),
+        with _on(q.device):
+            sc = self._any(self._bytes(cfg.chunk_scratch_bytes, self.nseq, int(max_new)))
+            _check(lib().kivi_chunk_attn(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(k_ptrs),
                                          _ptr(v_ptrs), _ptr(n_new), int(max_new), _ptr(q), _ptr(q_start), _ptr(out),
                                          float(scale), int(window), int(sinks), mkl, _ptr(sc), sc.numel(),
                                          _ptr(self.status), _stream(q.device)), "kivi_chunk_attn")
@@ -554,9 +581,9 @@ class KVCache:
         _require(weights, "weights", (self.nseq, stride), torch.float32, self.device)
         if stride * cfg.group < self.max_len:
             raise ValueError(f"weights must have a column for each of {-(-self.max_len // cfg.group)} groups")
-        with torch.cuda.device(weights.device):
-            sc = self._any(int(lib().kivi_evict_scratch_bytes(self.nseq, stride)))
-            _check(lib().kivi_evict_groups(cfg.c(), self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(weights),
+        with _on(weights.device):
+            sc = self._any(self._bytes(_evict_scratch_bytes, self.nseq, stride))
+            _check(lib().kivi_evict_groups(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(weights),
                                            stride, int(keep_groups), int(sink_groups), int(recent_groups), _ptr(sc),
                                            sc.numel(), _ptr(self.status), _stream(weights.device)), "kivi_evict_groups")
         self.max_len = min(self.max_len, keep_groups * cfg.group + cfg.ring - 1)

@@ -56,7 +56,7 @@ static_assert(kSoftmaxRegs >= kLaunchRegs && kOperandRegs <= kLaunchRegs && kIss
               "setmaxnreg.inc must not lower a count, nor setmaxnreg.dec raise one");
 static_assert(256 * kSoftmaxRegs + 256 * kOperandRegs + 128 * kIssueRegs <= kChunkThreads * kLaunchRegs, "shares of the launch's registers");
 constexpr int kUnitOverhead = 3;          // units charged per (row tile pair, kv head)
-constexpr int kMinChunkUnits = 4;
+constexpr int kMinChunkUnits = 2;
 constexpr float kLag = 8.0f;              // log2 by which the softmax reference may lag behind
 
 // ---------------------------------------------------------------- mbarrier, tcgen05

@@ -128,6 +128,14 @@ __device__ __forceinline__ float exp2_ftz(float x) {
     return y;
 }
 
+// x += y for four floats, two at a time
+__device__ __forceinline__ void add4(float (&x)[4], const float (&y)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+        asm("{ .reg .b64 a, b; mov.b64 a, {%0, %1}; mov.b64 b, {%2, %3}; add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+            : "+f"(x[i]), "+f"(x[i + 1]) : "f"(y[i]), "f"(y[i + 1]));
+}
+
 // Codes at bits I*BITS and 16 + I*BITS of w as an exact f16 pair (low, high half).
 // The field is OR-ed into the mantissa of 1024.0 and the 1024 removed by one fma
 // (the field's position scaled away by a power of two); fields that reach past the
@@ -468,23 +476,28 @@ __device__ __forceinline__ float* segment_record(const DecodeArgs& a, const Stre
 // Thread d owns channel d of every head and folds the records in one pass with the
 // log-sum-exp rescaling (a record with a larger max rescales what came before), so the loads
 // of all records are independent of one another.
-template <int GQ>
-__device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSegs& ss, float* out_s, int nh = GQ,
-                                             float* lse = nullptr) {
+// In the extended modes a CTA may have N = 1 head (h0) of the GQ that a record holds: with few
+// streams split over many CTAs (three sequences of up to 9001 tokens, 4 kv heads of 7 query
+// heads) one CTA for all of a stream's heads took longer than the attention, 39 us against 37;
+// with more streams than kMergeCtas / GQ the extra CTAs' plans cost more than they gain (512
+// streams of 4 heads: 119 against 113 us for the whole call). Only heads below nh are real.
+template <int GQ, int N = GQ>
+__device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSegs& ss, float* out_s, int h0 = 0,
+                                             int nh = GQ, float* lse = nullptr) {
     static_assert(kThreads == kD, "one thread per channel");
     const int d = threadIdx.x;
-    float M[GQ], den[GQ], num[GQ];
+    float M[N], den[N], num[N];
 #pragma unroll
-    for (int hh = 0; hh < GQ; ++hh) {
+    for (int hh = 0; hh < N; ++hh) {
         M[hh] = -CUDART_INF_F;
         den[hh] = 0.0f;
         num[hh] = 0.0f;
     }
-#pragma unroll 4
+#pragma unroll (N == 1 ? 8 : 4)
     for (int k = 0; k < ss.nseg; ++k) {
 #pragma unroll
-        for (int hh = 0; hh < GQ; ++hh) {
-            const float* r = segment_record<GQ>(a, ss, k, hh);
+        for (int hh = 0; hh < N; ++hh) {
+            const float* r = segment_record<GQ>(a, ss, k, h0 + hh);
             const float mk = __ldcg(r + kD), lk = __ldcg(r + kD + 1), xk = __ldcg(r + d);
             if (mk == -CUDART_INF_F) continue;   // an empty segment adds nothing
             const float Mn = fmaxf(M[hh], mk);
@@ -495,18 +508,17 @@ __device__ __forceinline__ void merge_stream(const DecodeArgs& a, const StreamSe
         }
     }
 #pragma unroll
-    for (int hh = 0; hh < GQ; ++hh) {
-        if (hh < nh) {
-            out_s[hh * kD + d] = num[hh] / den[hh];
-            if (lse != nullptr && d == 0) lse[hh] = M[hh] + log2f(den[hh]);
-        }
+    for (int hh = 0; hh < N; ++hh) {
+        if (h0 + hh >= nh) continue;
+        out_s[(h0 + hh) * kD + d] = num[hh] / den[hh];
+        if (lse != nullptr && d == 0) lse[h0 + hh] = M[hh] + log2f(den[hh]);
     }
-    // the stream's records back to zero (each segment's GQ records are contiguous) once every
+    // the stream's records back to zero (a segment's records of these heads are contiguous) once every
     // thread has read them
     __syncthreads();
     for (int k = 0; k < ss.nseg; ++k) {
-        float4* z = reinterpret_cast<float4*>(segment_record<GQ>(a, ss, k, 0));
-        for (int i = d; i < GQ * (kD + 4) / 4; i += kThreads) z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float4* z = reinterpret_cast<float4*>(segment_record<GQ>(a, ss, k, h0));
+        for (int i = d; i < N * (kD + 4) / 4; i += kThreads) z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
 }
 
@@ -927,6 +939,8 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
     const int vbyte = VB == 2 ? 4 * (gid >> 2) : 4 * (gid >> 1);   // byte offset of the word in a 32-channel block
     const uint32_t sel_z = (gid & 1) ? 0x7632u : 0x5410u;
 
+    float2* stats = X && a.stats != nullptr ? tile_stats(a, b, 0, head0) + t : nullptr;   // head t's, tile 0
+
     float m_run = -CUDART_INF_F, l_run = 0.0f;
     float cv[8][4], cz[4];
 #pragma unroll
@@ -1071,12 +1085,12 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
         const float psum = (p[0] + p[1]) + (p[2] + p[3]);
         l_run += psum;
         if constexpr (X) {
-            if (a.stats != nullptr) {
+            if (stats != nullptr) {
                 float ts = psum;
                 ts += __shfl_xor_sync(kFull, ts, 4);
                 ts += __shfl_xor_sync(kFull, ts, 8);
                 ts += __shfl_xor_sync(kFull, ts, 16);
-                if (gid == 0 && t < nh) tile_stats(a, b, tile_of(it), head0)[t] = make_float2(m_run, ts);
+                if (gid == 0 && t < nh) stats[static_cast<int64_t>(tile_of(it)) * a.Hq] = make_float2(m_run, ts);
             }
         }
 #pragma unroll
@@ -1155,11 +1169,8 @@ __device__ __forceinline__ void group_segment(const DecodeArgs& a, const MmaSmem
                 float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) value_mma(k2, kg, u0, u1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    cv[2 * kg][i] += u0[i];
-                    cv[2 * kg + 1][i] += u1[i];
-                }
+                add4(cv[2 * kg], u0);
+                add4(cv[2 * kg + 1], u1);
             }
         } else {
 #pragma unroll
@@ -1568,11 +1579,8 @@ __device__ __forceinline__ void group_segment8(const DecodeArgs& a, const MmaSme
                 float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int k2 = 0; k2 < 2; ++k2) value_mma(k2, kg, u0, u1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    cv[2 * kg][i] += u0[i];
-                    cv[2 * kg + 1][i] += u1[i];
-                }
+                add4(cv[2 * kg], u0);
+                add4(cv[2 * kg + 1], u1);
             }
         } else {
 #pragma unroll
@@ -1823,12 +1831,18 @@ __global__ void __launch_bounds__(kThreads) decode_merge_kernel(DecodeArgs a, in
         if (ss.nseg < 2) continue;
         asm volatile("griddepcontrol.wait;" ::: "memory");   // returns at once after the first time
         const int64_t row = stream_row<GQ, MQ>(a, b, h);
-        if constexpr (MQ == kExtended)
-            merge_stream<GQ>(a, ss, a.out + row * kD, stream_heads<GQ, MQ>(a, h),
-                             a.lse == nullptr ? nullptr : a.lse + row);
-        else
+        if constexpr (MQ == kExtended) {
+            const int nh = stream_heads<GQ, MQ>(a, h);
+            float* lse = a.lse == nullptr ? nullptr : a.lse + row;
+            if (gridDim.y == 1) merge_stream<GQ>(a, ss, a.out + row * kD, 0, nh, lse);
+            else merge_stream<GQ, 1>(a, ss, a.out + row * kD, blockIdx.y, nh, lse);
+        } else {
             merge_stream<GQ>(a, ss, a.out + row * kD);
+        }
     }
+    // the kernel behind this one (weights per group) waits for this grid alone, so this grid must not
+    // end before the decode grid has
+    if constexpr (MQ == kExtended) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int KB, int VB, int DT, int GQ, int G, int MQ = 0>
@@ -1842,7 +1856,7 @@ cudaError_t launch_mma(const DecodeArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int64_t S = static_cast<int64_t>(a.nseq) * a.H * (MQ == kExtended ? a.n_part : MQ ? a.n_query : 1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(S < kMergeCtas ? S : kMergeCtas));
+    cfg.gridDim = dim3(static_cast<unsigned>(S < kMergeCtas ? S : kMergeCtas), MQ == kExtended && S * GQ <= kMergeCtas ? GQ : 1);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.stream = stream;

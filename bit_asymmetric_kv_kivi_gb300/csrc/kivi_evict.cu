@@ -21,41 +21,56 @@ constexpr unsigned kAll = 0xffffffffu;
 // ---------------------------------------------------------------- weights per group
 
 constexpr int kWeightWarps = 8;
+constexpr int kWeightGroups = 4;   // groups of a warp: their loads are in flight together
 
-// One warp per (sequence, group): lanes over query heads, then a butterfly sum (a fixed order,
-// so the result does not depend on timing).
+// One warp per (sequence, kWeightGroups groups): lanes over query heads, then a butterfly sum (a fixed
+// order, so the result does not depend on timing). Launched behind the merge kernel as a
+// programmatic dependent.
 __global__ void __launch_bounds__(kWeightWarps * 32) group_weights_kernel(GroupWeightArgs a) {
     const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int j = blockIdx.x * kWeightWarps + (threadIdx.x >> 5);
-    if (j >= a.stride) return;
-    const int64_t at = static_cast<int64_t>(b) * a.stride + j;
+    const int j0 = (blockIdx.x * kWeightWarps + (threadIdx.x >> 5)) * kWeightGroups;
     const int64_t L = a.kv_len[b];
-    const float before = a.in != nullptr ? a.in[at] : 0.0f;
-    if (L < 0 || L > a.max_kv_len || n_packed(L, a.R, a.G) > a.seqs[b].cap_tokens) {   // a bad length (status set by the decode kernel)
-        if (lane == 0) a.out[at] = before;
-        return;
-    }
-    if (static_cast<int64_t>(j) * a.G >= L) {
-        if (lane == 0) a.out[at] = 0.0f;
-        return;
-    }
-    const int tpg = a.G / kTile;
-    const int t0 = j * tpg, tiles = static_cast<int>((L + kTile - 1) / kTile);
-    const float2* st = a.stats + (static_cast<int64_t>(b) * a.max_tiles + t0) * a.Hq;
-    float w = 0.0f;
-    for (int t = 0; t < tpg && t0 + t < tiles; ++t)
-        for (int h = lane; h < a.Hq; h += 32) {
-            const float2 x = st[static_cast<int64_t>(t) * a.Hq + h];
-            w = fmaf(x.y, exp2f(x.x - a.lse[static_cast<int64_t>(b) * a.Hq + h]), w);
-        }
+    const bool bad = L < 0 || L > a.max_kv_len || n_packed(L, a.R, a.G) > a.seqs[b].cap_tokens;   // (status set by the decode kernel)
+    const int tpg = a.G / kTile, tiles = bad ? 0 : static_cast<int>((L + kTile - 1) / kTile);
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // before anything an earlier kernel writes, weights included
+    if (j0 >= a.stride) return;
+    const float2* st = a.stats + (static_cast<int64_t>(b) * a.max_tiles + static_cast<int64_t>(j0) * tpg) * a.Hq;
+    float w[kWeightGroups];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(kAll, w, o);
-    if (lane == 0) a.out[at] = a.in != nullptr && a.decay != 0.0f ? fmaf(a.decay, before, w) : w;
+    for (int g = 0; g < kWeightGroups; ++g) w[g] = 0.0f;
+    for (int h = lane; h < a.Hq; h += 32) {
+        const float lse = a.lse[static_cast<int64_t>(b) * a.Hq + h];
+#pragma unroll
+        for (int i = 0; i < 2 * kWeightGroups; ++i) {   // tiles of these groups (half as many when G = 32)
+            if (i < tpg * kWeightGroups && j0 * tpg + i < tiles) {
+                const float2 x = st[static_cast<int64_t>(i) * a.Hq + h];
+                const float y = x.y * exp2f(x.x - lse);
+                w[i >> 1] += tpg == 2 ? y : 0.0f;
+                if (i < kWeightGroups) w[i] += tpg == 1 ? y : 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < kWeightGroups; ++g) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w[g] += __shfl_xor_sync(kAll, w[g], o);
+    }
+    if (lane < kWeightGroups && j0 + lane < a.stride) {
+        const int j = j0 + lane;
+        const int64_t at = static_cast<int64_t>(b) * a.stride + j;
+        float v = w[0];
+#pragma unroll
+        for (int g = 1; g < kWeightGroups; ++g) v = lane == g ? w[g] : v;
+        const bool held = static_cast<int64_t>(j) * a.G < L;
+        const float before = a.in != nullptr && (bad || (held && a.decay != 0.0f)) ? a.in[at] : 0.0f;
+        a.out[at] = bad ? before : !held ? 0.0f : a.decay != 0.0f ? fmaf(a.decay, before, v) : v;
+    }
 }
 
 // ---------------------------------------------------------------- eviction
 
 constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 8192;    // groups whose keys are kept in shared memory between the passes
 constexpr int kSelWarps = kSelThreads / 32;
 
 // Weights as unsigned numbers of the same order; NaN below everything, the zeros equal.
@@ -98,6 +113,7 @@ __device__ __forceinline__ uint32_t scan_pair(uint32_t v, uint32_t* s, uint32_t*
 //      entries before it writes any, and writes none past the block, so no entry is lost.
 __global__ void __launch_bounds__(kSelThreads) group_select_kernel(EvictArgs a) {
     __shared__ uint32_t hist[256];
+    __shared__ uint32_t s_keys[kSelKeys];
     __shared__ uint32_t s_scan[kSelWarps];
     __shared__ uint32_t s_key, s_need;
     const int tid = threadIdx.x, b = blockIdx.x;
@@ -123,12 +139,15 @@ __global__ void __launch_bounds__(kSelThreads) group_select_kernel(EvictArgs a) 
 
     uint32_t key = 0, need = static_cast<uint32_t>(a.keep - a.sink - a.recent);
     if (need > 0) {
-        // the need-th largest key among the candidates
+        // the need-th largest key among the candidates (their keys read from memory once, where they fit)
+        const bool cached = c1 - c0 <= kSelKeys;
+        if (cached)
+            for (int j = c0 + tid; j < c1; j += kSelThreads) s_keys[j - c0] = weight_key(w[j]);
         for (int shift = 24; shift >= 0; shift -= 8) {
             for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
             __syncthreads();
             for (int j = c0 + tid; j < c1; j += kSelThreads) {
-                const uint32_t k = weight_key(w[j]);
+                const uint32_t k = cached ? s_keys[j - c0] : weight_key(w[j]);   // this thread's own entry
                 if (shift == 24 || (k >> (shift + 8)) == (key >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1u);
             }
             __syncthreads();
@@ -214,6 +233,7 @@ __global__ void __launch_bounds__(kSelThreads) group_select_kernel(EvictArgs a) 
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 16;   // groups in flight per thread
+constexpr int kTurnBatch = 10;   // ring rows in flight per thread
 constexpr int kTurnSmem = 40 * 1024;
 
 // Grid (tasks, kv heads, sequences). Tasks [0, 2 slices) turn one slice of 16-byte columns of
@@ -235,13 +255,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, i
         const int cols = a.D * 2 / 16;   // 16-byte columns of a row
         const int s0 = (blockIdx.x >> 1) * slice, w = cols - s0 < slice ? cols - s0 : slice;
         uint4* base = static_cast<uint4*>((blockIdx.x & 1) ? sq.v_res : sq.k_res) + static_cast<int64_t>(h) * ring * cols + s0;
+        // (slice is a power of two that divides the block, so a thread stays in one column)
         uint4* buf = reinterpret_cast<uint4*>(smem);
-        for (int i = tid; i < ring * w; i += kMoveThreads) buf[i] = base[static_cast<int64_t>(i / w) * cols + i % w];
+        const int col = tid % slice, step = kMoveThreads / slice;
+        if (col < w)
+            for (int row = tid / slice; row < ring; row += step * kTurnBatch) {
+                uint4 v[kTurnBatch];
+#pragma unroll
+                for (int i = 0; i < kTurnBatch; ++i)
+                    if (row + i * step < ring) v[i] = base[static_cast<int64_t>(row + i * step) * cols + col];
+#pragma unroll
+                for (int i = 0; i < kTurnBatch; ++i)
+                    if (row + i * step < ring) buf[(row + i * step) * slice + col] = v[i];
+            }
         __syncthreads();
-        for (int i = tid; i < ring * w; i += kMoveThreads) {
-            const int row = i / w, from = row + turn < ring ? row + turn : row + turn - ring;
-            base[static_cast<int64_t>(row) * cols + i % w] = buf[from * w + i % w];
-        }
+        if (col < w)
+#pragma unroll 4
+            for (int row = tid / slice; row < ring; row += step) {
+                const int from = row + turn < ring ? row + turn : row + turn - ring;
+                base[static_cast<int64_t>(row) * cols + col] = buf[from * slice + col];
+            }
         return;
     }
     if (seq_paged(sq)) return;
@@ -279,9 +312,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a, i
 }  // namespace
 
 cudaError_t launch_group_weights(const GroupWeightArgs& a, cudaStream_t stream) {
-    const dim3 grid((a.stride + kWeightWarps - 1) / kWeightWarps, a.nseq);
-    group_weights_kernel<<<grid, kWeightWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    constexpr int per = kWeightWarps * kWeightGroups;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.stride + per - 1) / per, a.nseq);
+    cfg.blockDim = dim3(kWeightWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, group_weights_kernel, a);
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
@@ -290,7 +331,8 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int ring = a.R + a.G, cols = a.D * 2 / 16;
     int slice = kTurnSmem / (ring * 16);
-    slice = slice < 1 ? 1 : slice > cols ? cols : slice;
+    while (slice & (slice - 1)) slice &= slice - 1;   // a power of two
+    slice = slice < 1 ? 1 : slice > 32 ? 32 : slice;
     const int n_slices = (cols + slice - 1) / slice;
     const int smem = ring * slice * 16;
     if (smem > 48 * 1024) {
