@@ -455,16 +455,17 @@ struct ChunkStored {
     int L, end;   // cached tokens; cached and new ones
     int ring;
 };
-// The four rows of a lane of the stored subtile at token tb; rows behind the last token are zeros.
+// One row of a lane's span at token t; a row behind the last token is zeros.
+__device__ __forceinline__ void load_row(const ChunkStored& s, int t, int span, uint32_t (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0;
+    if (t < s.L) load8(w, s.res + static_cast<int64_t>(t % s.ring) * kD + span * 16);
+    else if (t < s.end) load8(w, s.fresh + static_cast<int64_t>(t - s.L) * kD + span * 16);
+}
+// The four rows of a lane of the stored subtile at token tb.
 __device__ __forceinline__ void load_stored(const ChunkStored& s, int tb, int row_lo, int span, uint32_t (&w)[4][8]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int t = tb + row_lo + 8 * k;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[k][i] = 0;
-        if (t < s.L) load8(w[k], s.res + static_cast<int64_t>(t % s.ring) * kD + span * 16);
-        else if (t < s.end) load8(w[k], s.fresh + static_cast<int64_t>(t - s.L) * kD + span * 16);
-    }
+    for (int k = 0; k < 4; ++k) load_row(s, tb + row_lo + 8 * k, span, w[k]);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -886,8 +887,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                 src.res = static_cast<const uint16_t*>(VALUES ? sq.v_res : sq.k_res) + static_cast<int64_t>(s.h) * src.ring * kD;
                 src.fresh = static_cast<const uint16_t*>(VALUES ? a.v_new[s.it.b] : a.k_new[s.it.b]) +
                             static_cast<int64_t>(s.h) * s.it.n * kD;
-                const int x1 = s.x1, lst = s.it.st, skip = s.it.skip;
-                for (int j = s.x0; j < x1; ++j, ++n) {
+                const int x0 = s.x0, x1 = s.x1, lst = s.it.st, skip = s.it.skip;
+                if (np <= (x0 < lst ? x0 : x0 + skip) * kKeys) {
+                    // stored tokens only (a first chunk): as each row is stored, the row that follows it in the
+                    // next subtile is loaded in its place
+                    uint32_t x[4][8];
+                    load_stored(src, (x0 < lst ? x0 : x0 + skip) * kKeys + 2 * half * kTile, row_lo, span, x);
+                    for (int j = x0; j < x1; ++j, ++n) {
+                        const uint32_t st = n % kKvStages, use = n / kKvStages;
+                        const int t0 = (j < lst ? j : j + skip) * kKeys + 2 * half * kTile;
+                        const int t1 = (j + 1 < lst ? j + 1 : j + 1 + skip) * kKeys + 2 * half * kTile;   // in the next tile
+                        if (use > 0) ok = warp_wait(smem_u32(&empty[st]), (use - 1) & 1, stop);
+                        if (!ok) break;
+                        unsigned char* dst = tiles + st * kOpBytes + half * (2 * kTile * 128);
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i, dst += kTile * 128) {
+                            const int next = i == 0 ? t0 + kTile : j + 1 < x1 ? t1 : src.end;   // (rows from end on are zeros)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t o[8];
+                                pair_stored<BITS, DT>(x[k], o);
+                                *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(o[0], o[1], o[2], o[3]);
+                                *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(o[4], o[5], o[6], o[7]);
+                                load_row(src, next + row_lo + 8 * k, span, x[k]);
+                            }
+                        }
+                        proxy_fence();
+                        warp_arrive(smem_u32(&full[st]));
+                    }
+                    continue;
+                }
+                for (int j = x0; j < x1; ++j, ++n) {
                     const uint32_t st = n % kKvStages, use = n / kKvStages;
                     const int t0 = (j < lst ? j : j + skip) * kKeys;
                     const int packed = np <= t0 ? 0 : np - t0 >= kKeys ? kKeys / kTile : (np - t0) / kTile;   // subtiles

@@ -108,6 +108,59 @@ def test_evict_other_head_dims_and_rings(D, G, R):
         assert np.array_equal(wd[b].cpu().numpy(), want_w, equal_nan=True)
 
 
+def test_evict_very_long_sequence():
+    """More groups than the selection keeps in shared memory."""
+    D, G, R, n = 32, 32, 32, 9001
+    cfg = kivi.Config(head_dim=D, residual=R, group=G)
+    cache = kivi.KVCache(cfg, 1, n * G, paged=True, page_seed=1)
+    L = R + n * G + 3
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache.append(torch.randn((1, 1, L, D), generator=gen, device="cuda").half(),
+                 torch.randn((1, 1, L, D), generator=gen, device="cuda").half())
+    before, table = cache.seq_numpy(0), cache.block_tables[0].cpu().numpy()
+    for keep, kind in ((8800, "wide"), (300, "ties")):
+        w = weights_for(cache, kind, keep)
+        wd = torch.from_numpy(w).cuda()
+        kept, gone, want_w, turn = evict(oracle.Cfg(group=G, residual=R), w[0], before["kv_len"], keep, 3, 5)
+        cache.evict(wd, keep, 3, 5)
+        same(cache.seq_numpy(0), expect(before, cfg, kept, turn))
+        assert np.array_equal(wd[0].cpu().numpy(), want_w, equal_nan=True)
+        got = cache.block_tables[0].cpu().numpy()
+        assert np.array_equal(got[:keep], table[kept]) and sorted(got) == sorted(table)
+        before, table = cache.seq_numpy(0), got
+    assert int(cache.status.item()) == 0
+
+
+def test_cache_over_given_buffers():
+    """KVCache.from_buffers reads and writes the caller's tensors; tensors that do not fit are refused."""
+    wl = synth.Workload("given", 2, 4, 2, 128, (700, 161), "f16", seed=6)
+    cache, refs = build(wl, 2, 2, 32, 128, 704, paged=True)
+    buf = {n: getattr(cache, n) for n in kivi.SEQ_FIELDS}
+    args = (cache.cfg, buf, cache.kv_len, 704)
+    other = kivi.KVCache.from_buffers(*args, block_tables=cache.block_tables, max_len=700)
+    q = dev_tensor(wl.query(0), "f16")
+    assert torch.equal(other.decode_window(q, 300, 4), cache.decode_window(q, 300, 4))
+    w = torch.rand((2, other.weight_groups()), device="cuda")
+    other.evict(w, 5)
+    assert other.max_len == 5 * 32 + 159 and int(cache.kv_len[0]) == 700 - (17 - 5) * 32
+    halves = {n: t.view(torch.float16) if t.dtype == torch.int16 else t for n, t in buf.items()}
+    kivi.KVCache.from_buffers(cache.cfg, halves, cache.kv_len, 704, block_tables=cache.block_tables)
+    for name in kivi.SEQ_FIELDS:
+        for bad in (buf[name][:, :1], buf[name].float(), buf[name].cpu()):
+            with pytest.raises(ValueError):
+                kivi.KVCache.from_buffers(cache.cfg, {**buf, name: bad}, cache.kv_len, 704, block_tables=cache.block_tables)
+    with pytest.raises(ValueError):
+        kivi.KVCache.from_buffers(cache.cfg, buf, cache.kv_len, 700, block_tables=cache.block_tables)
+    with pytest.raises(ValueError):
+        kivi.KVCache.from_buffers(cache.cfg, buf, cache.kv_len, 704, block_tables=cache.block_tables[:, :4])
+    with pytest.raises(ValueError):
+        other.decode_window(q, 300, out=torch.empty((2, 4, 128), device="cuda", dtype=torch.float16))
+    with pytest.raises(ValueError):
+        other.decode_window(q.bfloat16(), 300)
+    with pytest.raises(ValueError):
+        other.decode_weights(q, w.double())
+
+
 def test_evict_refusals_leave_the_cache_alone():
     wl = synth.Workload("refuse", 2, 2, 2, 128, (1000, 500), "f16", seed=5)
     cache, _ = build(wl, 2, 2, 32, 128, 1024)
