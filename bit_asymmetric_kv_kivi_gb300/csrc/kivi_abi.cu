@@ -349,6 +349,7 @@ kivi_status kivi_chunk_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* s
     kivi::ChunkArgs a;
     size_t rec;
     kivi::chunk_plan(cfg->num_q_heads, cfg->num_kv_heads, max_new, &a.pairs, &a.rec_tiles, &rec);
+    if (static_cast<int64_t>(a.pairs) * nseq > INT32_MAX) return KIVI_ERR_UNSUPPORTED;
     a.kb = cfg->k_bits;
     a.vb = cfg->v_bits;
     a.G = cfg->group;

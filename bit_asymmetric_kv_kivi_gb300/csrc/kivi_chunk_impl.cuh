@@ -225,10 +225,10 @@ __device__ __forceinline__ bool chunk_seq(const ChunkArgs& a, int b, int64_t* L,
     return *L >= 0 && *L <= a.max_kv_len && n_packed(*L, a.R, a.G) <= a.seqs[b].cap_tokens;
 }
 
-__device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int64_t idx) {
+__device__ __forceinline__ ChunkItem chunk_item(const ChunkArgs& a, int idx) {
     ChunkItem it;
-    it.b = static_cast<int>(idx / a.pairs);
-    const int64_t row0 = (idx - static_cast<int64_t>(it.b) * a.pairs) * (2 * kRows);
+    it.b = idx / a.pairs;
+    const int64_t row0 = static_cast<int64_t>(idx - it.b * a.pairs) * (2 * kRows);
     const int g = a.Hq / a.H;
     it.nt = it.st = it.skip = it.rows = 0;
     it.row0 = 0;
@@ -260,9 +260,9 @@ __device__ __forceinline__ int64_t item_units(const ChunkItem& it) { return it.n
 // A CTA's share of the row of units; chunk_next yields its segments (a row tile pair of one kv
 // head, listed key tiles [x0, x1)).
 struct ChunkWalk {
-    int64_t lo, hi, pos, idx;   // this CTA's units, first unit of item idx
+    int64_t lo, hi, pos;        // this CTA's units, first unit of item idx
     int64_t U;
-    int C, h;
+    int idx, C, h;
 };
 struct ChunkSeg {
     ChunkItem it;
@@ -271,7 +271,7 @@ struct ChunkSeg {
 };
 
 __device__ __forceinline__ bool chunk_next(const ChunkArgs& a, ChunkWalk& w, ChunkSeg& s) {
-    const int64_t items = static_cast<int64_t>(a.nseq) * a.pairs;
+    const int items = a.nseq * a.pairs;   // below 2^31, by the entry point
     while (w.idx < items && w.pos < w.hi) {
         s.it = chunk_item(a, w.idx);
         const int64_t u = item_units(s.it);
@@ -315,8 +315,8 @@ struct ChunkShared {
     ChunkSeg seg[kSegs];
     float hand_m[kRows], hand_l[kRows];   // state of the second softmax warpgroup at the end of a narrow segment
     int64_t warp_sum[kChunkThreads / 32];
-    int64_t lo, hi, pos, idx, U;
-    int C, h;
+    int64_t lo, hi, pos, U;
+    int idx, C, h;
     uint32_t tmem;
     int stop;
 };
@@ -383,11 +383,6 @@ __device__ __forceinline__ void load8(uint32_t (&w)[8], const void* p) {
     const uint4 a = __ldg(q), b = __ldg(q + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-}
-
-__device__ __forceinline__ void store_rows(unsigned char* dst, int row, int span, const uint32_t (&o)[8]) {
-    *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span)) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(dst + op_addr(row, 2 * span + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // A warp's part of a packed subtile (32 tokens): lane (row_lo = lane % 8, span) has rows row_lo + 8 k of
@@ -547,7 +542,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
         mbar_init(smem_u32(&sh.hand_full), 4);
         mbar_init(smem_u32(&sh.hand_empty), 4);
         sh.stop = 0;
-        sh.idx = INT64_MAX;
+        sh.idx = INT32_MAX;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 16) {
@@ -556,11 +551,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     }
 
     // units of each thread's run of items, their exclusive prefix and the total
-    const int64_t items = static_cast<int64_t>(a.nseq) * a.pairs;
-    const int64_t per = (items + kChunkThreads - 1) / kChunkThreads;
-    const int64_t i0 = tid * per < items ? tid * per : items, i1 = i0 + per < items ? i0 + per : items;
+    const int items = a.nseq * a.pairs, per = (items + kChunkThreads - 1) / kChunkThreads;
+    const int i0 = static_cast<int>(static_cast<int64_t>(tid) * per < items ? static_cast<int64_t>(tid) * per : items);
+    const int i1 = items - i0 < per ? items : i0 + per;
     int64_t mine = 0;
-    for (int64_t i = i0; i < i1; ++i) mine += item_units(chunk_item(a, i)) * a.H;
+    for (int i = i0; i < i1; ++i) mine += item_units(chunk_item(a, i)) * a.H;
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -582,7 +577,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
         const int64_t lo = c * U / C, start = before + incl - mine;
         if (lo >= start && lo < start + mine) {
             int64_t p = start;
-            for (int64_t i = i0; i < i1; ++i) {
+            for (int i = i0; i < i1; ++i) {
                 const int64_t u = item_units(chunk_item(a, i));
                 if (lo < p + u * a.H) {
                     sh.lo = lo;
@@ -629,42 +624,77 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             const bool warp_live = tile * kRows + (r & ~31) < s.it.rows;     // some row of this warp is real
             const int qi = row / g;
             const int64_t qrow = (static_cast<int64_t>(a.q_start[s.it.b]) + qi) * a.Hq + s.h * g + (row - qi * g);
-            float sl;                                    // log2 units per score
+            float sl = 1.0f;        // log2 units per score of this thread's row
+            // This warp's 32 rows of Q, 16 lanes a row, scaled by a power of two to |q| in (1/2, 1], in K's channel
+            // order. (A lane per row took 12000 clocks a segment, this a third of it.)
             {
-                // the row of Q, scaled by a power of two to |q| in (1/2, 1], in K's channel order
-                const uint16_t* q = static_cast<const uint16_t*>(a.q) + qrow * kD;
-                float mx = 0.0f;
-#pragma unroll 2
-                for (int sp = 0; sp < 8; ++sp) {
-                    uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (live) load8(x, q + sp * 16);
+                const int chunk = lane & 15, base = s.it.row0 + tile * kRows + (r & ~31), end = s.it.row0 + s.it.rows;
+                const int64_t q0 = static_cast<int64_t>(a.q_start[s.it.b]) * a.Hq + s.h * g;   // the first query's first head
+                unsigned char* qt = sq_tile + tile * kOpBytes;
+                int e_mine = 0;
+                int row_k = base + (lane >> 4), qk = row_k / g, hk = row_k - qk * g;    // this lane's next row: query and head
+#pragma unroll 1
+                for (int k0 = 0; k0 < 16; k0 += 8) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mx = fmaxf(mx, fmaxf(fabsf(widen<DT>(static_cast<uint16_t>(x[i]))),
-                                             fabsf(widen<DT>(static_cast<uint16_t>(x[i] >> 16)))));
-                }
-                int e = 0;
-                if (mx > 0.0f && a.scale_log2 != 0.0f) frexpf(mx, &e);
-                const float pre = a.scale_log2 == 0.0f ? 0.0f : copysignf(ldexpf(1.0f, -e), a.scale_log2);
-                sl = a.scale_log2 == 0.0f ? 1.0f : ldexpf(fabsf(a.scale_log2), e);
-                if (wg == tile) {
-                    unsigned char* qt = sq_tile + tile * kOpBytes;
-#pragma unroll 2
-                    for (int sp = 0; sp < 8; ++sp) {
-                        uint32_t x[8] = {0, 0, 0, 0, 0, 0, 0, 0}, o[8];
-                        if (live) load8(x, q + sp * 16);
+                    for (int k = 0; k < 8; ++k) {
+                        x[k] = row_k < end ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                                  (q0 + static_cast<int64_t>(qk) * a.Hq + hk) * kD) + chunk)
+                                           : make_uint4(0, 0, 0, 0);
+                        row_k += 2;
+                        hk += 2;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c0 = span_channel<KB>(2 * i), c1 = span_channel<KB>(2 * i + 1);
-                            const float x0 = widen<DT>(static_cast<uint16_t>((c0 & 1) ? x[c0 >> 1] >> 16 : x[c0 >> 1]));
-                            const float x1 = widen<DT>(static_cast<uint16_t>((c1 & 1) ? x[c1 >> 1] >> 16 : x[c1 >> 1]));
-                            o[i] = pack_h2(x0 * pre, x1 * pre);
-                        }
-                        store_rows(qt, r, sp, o);
+                        for (int i = 0; i < 2; ++i)
+                            if (hk >= g) {
+                                hk -= g;
+                                ++qk;
+                            }
                     }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        float mx = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mx = fmaxf(mx, fmaxf(fabsf(widen<DT>(static_cast<uint16_t>(w[i]))), fabsf(widen<DT>(static_cast<uint16_t>(w[i] >> 16)))));
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+                        // 2^e above mx (from its exponent field; a zero row takes any), kept where 2^e and 2^-e are normal
+                        int e = static_cast<int>(__float_as_uint(mx) >> 23) - 126;
+                        e = e < -126 ? -126 : e > 126 ? 126 : e;
+                        const float pre = a.scale_log2 == 0.0f ? 0.0f : copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), a.scale_log2);
+                        const int rk = (r & ~31) + 2 * (k0 + k) + (lane >> 4);
+                        const int e_row = __shfl_sync(kFull, e, 16 * (lane & 1));   // of row 2 (k0 + k) + (lane & 1)
+                        if (lane >> 1 == k0 + k) e_mine = e_row;
+                        if (wg != tile) continue;      // a narrow segment's second warpgroup: the tile is the first's to fill
+                        uint32_t f[4], o[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            f[i] = pack_h2(widen<DT>(static_cast<uint16_t>(w[i])) * pre, widen<DT>(static_cast<uint16_t>(w[i] >> 16)) * pre);
+                        if constexpr (KB == 2) {
+                            // pairs (i, i + 8) of 16 channels: this lane has eight of them, its neighbour the others
+                            const bool upper = chunk & 1;
+                            const uint32_t g0 = __shfl_xor_sync(kFull, upper ? f[0] : f[2], 1), g1 = __shfl_xor_sync(kFull, upper ? f[1] : f[3], 1);
+                            const uint32_t a0 = upper ? g0 : f[0], a1 = upper ? g1 : f[1], b0 = upper ? f[2] : g0, b1 = upper ? f[3] : g1;
+                            o[0] = prmt(a0, b0, 0x5410u);
+                            o[1] = prmt(a0, b0, 0x7632u);
+                            o[2] = prmt(a1, b1, 0x5410u);
+                            o[3] = prmt(a1, b1, 0x7632u);
+                        } else {
+                            o[0] = prmt(f[0], f[2], 0x5410u);   // pairs (i, i + 4) of eight channels
+                            o[1] = prmt(f[0], f[2], 0x7632u);
+                            o[2] = prmt(f[1], f[3], 0x5410u);
+                            o[3] = prmt(f[1], f[3], 0x7632u);
+                        }
+                        *reinterpret_cast<uint4*>(qt + op_addr(rk, chunk)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                if (wg == tile) {
                     proxy_fence();
                     warp_arrive(smem_u32(&sh.q_full[tile]));
                 }
+                __syncwarp();
+                if (a.scale_log2 != 0.0f) sl = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e_mine) << 23);
             }
             // tokens this row sees: [lo, pos] and [0, sinks)
             const int len = static_cast<int>(s.it.L), pos = len + qi;

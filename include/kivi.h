@@ -384,7 +384,8 @@ size_t kivi_decode_weights_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int3
  * v_new with magnitudes up to 65504 (the codec's domain), also in rows that no query sees.
  * Device error KIVI_ERR_LENGTH: n_new_b outside [0, max_new] (nothing is written for b), or kv_len_b outside [0,
  * max_kv_len] or more tokens than the sequence can hold (its output rows are NaN).
- * Errors: KIVI_ERR_ARG for a negative window, sinks or size; KIVI_ERR_UNSUPPORTED unless D == 128.
+ * Errors: KIVI_ERR_ARG for a negative window, sinks or size; KIVI_ERR_UNSUPPORTED unless D == 128, or for sizes whose
+ * positions or (query, head) rows pass 32 bits, or whose row tiles of all sequences do.
  */
 kivi_status kivi_chunk_attn(const kivi_cfg* cfg, int32_t nseq, const kivi_seq* seqs_dev, const int32_t* kv_len_dev,
                             const void* const* k_new_dev, const void* const* v_new_dev, const int32_t* n_new_dev,

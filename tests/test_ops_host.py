@@ -84,6 +84,7 @@ def test_unsupported(lib):
     assert window(lib, wide) == kivi.ERR_UNSUPPORTED and weights(lib, wide) == kivi.ERR_UNSUPPORTED
     cfg = kivi.Config(num_q_heads=8, num_kv_heads=2).c()
     assert chunk(lib, cfg, max_new=2 ** 30) == kivi.ERR_UNSUPPORTED     # (query, head) rows past 32 bits
+    assert chunk(lib, cfg, nseq=65535, max_new=2 ** 28) == kivi.ERR_UNSUPPORTED   # row tiles past 32 bits
     assert chunk(lib, cfg, mkl=2 ** 31 - 1) == kivi.ERR_UNSUPPORTED     # positions past 32 bits
     assert evict(lib, kivi.Config(residual=12800).c()) == kivi.ERR_UNSUPPORTED
 
