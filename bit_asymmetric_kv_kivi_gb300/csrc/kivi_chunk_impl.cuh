@@ -52,6 +52,7 @@ constexpr int kKvStages = 2;
 // the launch's 96 x 640, and the three shares add up to it.
 constexpr int kSoftmaxRegs = 120, kOperandRegs = 88, kIssueRegs = 64;
 constexpr int kLaunchRegs = 96;           // what the launch bounds leave a thread
+static_assert(kKvStages == 2, "the barriers' phases count pairs of tiles");
 static_assert(kSoftmaxRegs >= kLaunchRegs && kOperandRegs <= kLaunchRegs && kIssueRegs <= kLaunchRegs,
               "setmaxnreg.inc must not lower a count, nor setmaxnreg.dec raise one");
 static_assert(256 * kSoftmaxRegs + 256 * kOperandRegs + 128 * kIssueRegs <= kChunkThreads * kLaunchRegs, "shares of the launch's registers");
@@ -182,6 +183,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ uint32_t op_addr(int row, int chunk) {   // chunk of 8 channels, 0 .. 15
     return static_cast<uint32_t>((chunk >> 3) * (kRows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
+// Key stages. bf16: one key tile of 128 rows. f16: half a tile, 64 rows of each channel block, twice: the
+// keys' leading parts and, behind them, their rests (split_grid). Two stages either way.
+template <bool LO>
+struct KeyStage {
+    static constexpr int kBlock = (LO ? kHalf : kKeys) * 128;   // bytes of a 64-channel block
+    static constexpr int kRest = 2 * kBlock;                    // where the rests begin (LO)
+};
+template <bool LO>
+__device__ __forceinline__ uint32_t key_addr(int row, int chunk) {
+    return static_cast<uint32_t>((chunk >> 3) * KeyStage<LO>::kBlock + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
 // Shared-memory descriptors, 128-byte swizzle, as (low word, high word): K-major (Q, K) has rows of 8
 // every 1024 bytes; MN-major (V: channels contiguous) has 64-channel blocks every kRows * 128 bytes
 // and groups of 8 tokens every 1024. Only the low word's address changes from one product to the next.
@@ -309,7 +321,7 @@ constexpr int kSegs = 4;                  // segments announced ahead (warp 18 w
 constexpr int kSegReaders = 19;           // every warp but the walking one
 
 struct ChunkShared {
-    uint64_t k_full[kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
+    uint64_t k_full[2 * kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
     uint64_t q_full[2], s_full[4], p_full[4], o_step[4];   // all but the first: [softmax warpgroup][half]
     uint64_t raw_full[kRawMax], raw_empty[kRawMax], hand_full, hand_empty, seg_full[kSegs], seg_empty[kSegs];
     ChunkSeg seg[kSegs];
@@ -385,12 +397,46 @@ __device__ __forceinline__ void load8(uint32_t (&w)[8], const void* p) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// Splits scale and zero of two channels, s = sh + sl and z = zh + zl exactly, with sh and zh on a grid so
+// coarse that c sh + zh is an f16 number for every code c. Let 2^e <= max(|z|, |qmax s + z|) < 2^(e + 1). Adding and
+// taking away 1.5 * 2^(e + 2), whose last bit is worth 2^(e - 8), rounds s and z to multiples of 2^(e - 8); the
+// levels c sh + zh are then below 2^10 of those. A dequantized key is fma(c, sh, zh), exact, plus
+// fma(c, sl, zl), at most 2^(e - 5) and rounded at 2^-11 of that: together 2^-16 of the largest level
+// where one f16 number gives 2^-11. From 2^13 on, where the sums could overflow, sh = s and zh = z, one
+// rounding as with bf16.
+template <int BITS>
+__device__ __forceinline__ void split_grid(uint32_t s, uint32_t z, uint32_t& sh, uint32_t& zh, uint32_t& sl, uint32_t& zl) {
+    constexpr uint32_t kQmax = BITS == 2 ? 0x42004200u : 0x4B804B80u;   // 3 or 15
+    const uint32_t m = hmax2(z & 0x7fff7fffu, hfma2(kQmax, s, z) & 0x7fff7fffu);
+    const uint32_t big = (((m + 0x10001000u) & 0x80008000u) >> 15) * 0xffffu;   // halves from 2^13 on
+    const uint32_t c = (((m & 0x7C007C00u) + 0x08000800u) | 0x02000200u) & ~big;
+    sh = hsub2(hadd2(s, c), c);
+    zh = hsub2(hadd2(z, c), c);
+    sl = hsub2(s, sh);
+    zl = hsub2(z, zh);
+}
+
 // A warp's part of a packed subtile (32 tokens): lane (row_lo = lane % 8, span) has rows row_lo + 8 k of
 // one 16-channel span, k = 0 .. 3, so that the span's key scales are read and paired once for four rows and
 // the eight lanes of a store phase hit eight rows, whose chunks lie in distinct banks under the swizzle.
 // st: the raw stage, already at the lane's place (row_lo, span) of each part; dst: the operand tile at row
 // row_lo of the subtile, a0 and a1 the lane's chunk offsets; gsh = log2 G.
-template <int KB, int VB, bool VALUES>
+template <int KB, int VB, bool VALUES, bool LO>
 __device__ __forceinline__ void fill_packed(const unsigned char* st, int gsh, int row_lo, int span, unsigned char* dst, uint32_t a0,
                                             uint32_t a1) {
     using Raw = RawLayout<KB, VB>;
@@ -427,20 +473,45 @@ __device__ __forceinline__ void fill_packed(const unsigned char* st, int gsh, in
             z1[k] = *reinterpret_cast<const uint16_t*>(meta + ((8 * k) << vsh) + (Raw::kVz - Raw::kVs));
         }
     }
+    if constexpr (!VALUES && LO) {
+        // by eight channels (one chunk of the row), so that the split scales of both do not have to be held
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t c[8];
-        pair_codes<BITS>(w[k], c);
-        if constexpr (VALUES) {
-            const uint32_t s2 = prmt(s1[k], s1[k], 0x1010u), z2 = prmt(z1[k], z1[k], 0x1010u);
+        for (int p = 0; p < 2; ++p) {
+            uint32_t sh[4], zh[4], sl[4], zl[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], s2, z2);
-        } else {
+            for (int i = 0; i < 4; ++i) split_grid<BITS>(sc[4 * p + i], zr[4 * p + i], sh[i], zh[i], sl[i], zl[i]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], sc[i], zr[i]);
+            for (int k = 0; k < 4; ++k) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t c;
+                    if constexpr (BITS == 2) c = code_slot<2>(w[k][0], w[k][0] >> CodeShift<2>::kValue, 4 * p + i);
+                    else c = code_slot<4>(w[k][p], w[k][p] >> CodeShift<4>::kValue, i);
+                    hi[i] = hfma2(c, sh[i], zh[i]);
+                    lo[i] = hfma2(c, sl[i], zl[i]);
+                }
+                unsigned char* to = dst + (p == 0 ? a0 : a1) + 1024 * k;
+                *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(to + KeyStage<LO>::kRest) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         }
-        *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(c[0], c[1], c[2], c[3]);
-        *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(c[4], c[5], c[6], c[7]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t c[8];
+            pair_codes<BITS>(w[k], c);
+            if constexpr (VALUES) {
+                const uint32_t s2 = prmt(s1[k], s1[k], 0x1010u), z2 = prmt(z1[k], z1[k], 0x1010u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], s2, z2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = hfma2(c[i], sc[i], zr[i]);
+            }
+            *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(c[0], c[1], c[2], c[3]);
+            *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(c[4], c[5], c[6], c[7]);
+        }
     }
 }
 
@@ -498,6 +569,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
     unsigned char* sk_tile = smem + 2 * kOpBytes;                    // [kKvStages]
     unsigned char* sv_tile = sk_tile + kKvStages * kOpBytes;         // [kKvStages]
     using Raw = RawLayout<KB, VB>;
+    constexpr bool LO = DT == KIVI_F16;    // keys in two parts: an f16 output would show one's rounding, a bf16 one hardly does
     unsigned char* raw_ring = sv_tile + kKvStages * kOpBytes;        // [Raw::kStages] raw packed subtiles
     ChunkShared& sh = *reinterpret_cast<ChunkShared*>(raw_ring + Raw::kStages * Raw::kBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
@@ -517,7 +589,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
 
     if (tid == 0) {
         for (int i = 0; i < kKvStages; ++i) {
-            mbar_init(smem_u32(&sh.k_full[i]), 4);
+            // (f16: a stage has a barrier for even tiles and one for odd ones, so that an issuing warp that takes every
+            // other tile sees every phase of the one it waits for; a parity tells two neighbouring phases apart only)
+            mbar_init(smem_u32(&sh.k_full[2 * i]), LO ? 2 : 4);
+            mbar_init(smem_u32(&sh.k_full[2 * i + 1]), LO ? 2 : 4);
             mbar_init(smem_u32(&sh.k_empty[i]), 2);   // one per issuing warp
             mbar_init(smem_u32(&sh.v_full[i]), 4);
             mbar_init(smem_u32(&sh.v_empty[i]), 2);
@@ -900,11 +975,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             // warps 0 and 1 of the group take the first two subtiles of a tile, 2 and 3 the others; each warp has
             // half of the spans
             const int half = (warp >> 1) & 1, row_lo = lane & 7, span = (lane >> 3) + 4 * (warp & 1);
-            const uint32_t a0 = op_addr(row_lo, 2 * span), a1 = op_addr(row_lo, 2 * span + 1);
-            const int gsh = a.G == 64 ? 6 : 5;
             uint64_t* full = VALUES ? sh.v_full : sh.k_full;
             uint64_t* empty = VALUES ? sh.v_empty : sh.k_empty;
             unsigned char* tiles = VALUES ? sv_tile : sk_tile;
+            constexpr bool SPLIT = LO && !VALUES;      // a stage is half a tile, this warp pair's own
+            const uint32_t a0 = SPLIT ? key_addr<LO>(row_lo, 2 * span) : op_addr(row_lo, 2 * span);
+            const uint32_t a1 = SPLIT ? key_addr<LO>(row_lo, 2 * span + 1) : op_addr(row_lo, 2 * span + 1);
+            auto stage = [&](uint32_t n) -> uint32_t { return SPLIT ? half : n % kKvStages; };
+            auto use_of = [&](uint32_t n) -> uint32_t { return SPLIT ? n : n / kKvStages; };
+            auto full_of = [&](uint32_t n) { return smem_u32(&full[SPLIT ? 2 * half + (n & 1) : n % kKvStages]); };
+            auto place = [&](uint32_t st) { return tiles + st * kOpBytes + (SPLIT ? 0 : half * (2 * kTile * 128)); };
+            // a lane's row of stored values to its two chunks; the rest of a stored f16 key is zero
+            auto put = [&](unsigned char* to, const uint32_t (&o)[8]) {
+                *reinterpret_cast<uint4*>(to + a0) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(to + a1) = make_uint4(o[4], o[5], o[6], o[7]);
+                if constexpr (SPLIT) {
+                    *reinterpret_cast<uint4*>(to + a0 + KeyStage<LO>::kRest) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(to + a1 + KeyStage<LO>::kRest) = make_uint4(0, 0, 0, 0);
+                }
+            };
+            const int gsh = a.G == 64 ? 6 : 5;
             uint32_t n = 0, raw0 = 0, raw_par = 0;    // tiles so far; the tile's first raw stage and its parity
             for (uint32_t si = 0; ok && seg_next(si); seg_done(si), ++si) {
                 const ChunkSeg& s = sh.seg[si % kSegs];
@@ -924,12 +1014,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                     uint32_t x[4][8];
                     load_stored(src, (x0 < lst ? x0 : x0 + skip) * kKeys + 2 * half * kTile, row_lo, span, x);
                     for (int j = x0; j < x1; ++j, ++n) {
-                        const uint32_t st = n % kKvStages, use = n / kKvStages;
+                        const uint32_t st = stage(n), use = use_of(n);
                         const int t0 = (j < lst ? j : j + skip) * kKeys + 2 * half * kTile;
                         const int t1 = (j + 1 < lst ? j + 1 : j + 1 + skip) * kKeys + 2 * half * kTile;   // in the next tile
                         if (use > 0) ok = warp_wait(smem_u32(&empty[st]), (use - 1) & 1, stop);
                         if (!ok) break;
-                        unsigned char* dst = tiles + st * kOpBytes + half * (2 * kTile * 128);
+                        unsigned char* dst = place(st);
 #pragma unroll 1
                         for (int i = 0; i < 2; ++i, dst += kTile * 128) {
                             const int next = i == 0 ? t0 + kTile : j + 1 < x1 ? t1 : src.end;   // (rows from end on are zeros)
@@ -937,31 +1027,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t o[8];
                                 pair_stored<BITS, DT>(x[k], o);
-                                *reinterpret_cast<uint4*>(dst + a0 + 1024 * k) = make_uint4(o[0], o[1], o[2], o[3]);
-                                *reinterpret_cast<uint4*>(dst + a1 + 1024 * k) = make_uint4(o[4], o[5], o[6], o[7]);
+                                put(dst + 1024 * k, o);
                                 load_row(src, next + row_lo + 8 * k, span, x[k]);
                             }
                         }
                         proxy_fence();
-                        warp_arrive(smem_u32(&full[st]));
+                        warp_arrive(full_of(n));
                     }
                     continue;
                 }
                 for (int j = x0; j < x1; ++j, ++n) {
-                    const uint32_t st = n % kKvStages, use = n / kKvStages;
+                    const uint32_t st = stage(n), use = use_of(n);
                     const int t0 = (j < lst ? j : j + skip) * kKeys;
                     const int packed = np <= t0 ? 0 : np - t0 >= kKeys ? kKeys / kTile : (np - t0) / kTile;   // subtiles
                     auto wait_empty = [&]() {
                         if (use > 0) ok = warp_wait(smem_u32(&empty[st]), (use - 1) & 1, stop);
                     };
-                    unsigned char* dst = tiles + st * kOpBytes + half * (2 * kTile * 128);
+                    unsigned char* dst = place(st);
                     auto stored = [&](const uint32_t (&x)[4][8], unsigned char* to) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t o[8];
                             pair_stored<BITS, DT>(x[k], o);
-                            *reinterpret_cast<uint4*>(to + a0 + 1024 * k) = make_uint4(o[0], o[1], o[2], o[3]);
-                            *reinterpret_cast<uint4*>(to + a1 + 1024 * k) = make_uint4(o[4], o[5], o[6], o[7]);
+                            put(to + 1024 * k, o);
                         }
                     };
                     if (2 * half < packed) {
@@ -975,7 +1063,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                         const int subs = packed - 2 * half < 2 ? 1 : 2;
 #pragma unroll 1
                         for (int i = 0; i < subs; ++i) {
-                            fill_packed<KB, VB, VALUES>(from, gsh, row_lo, span, dst, a0, a1);
+                            fill_packed<KB, VB, VALUES, LO>(from, gsh, row_lo, span, dst, a0, a1);
                             from += Raw::kSub;
                             dst += kTile * 128;
                         }
@@ -1000,7 +1088,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                         raw_par ^= 1;
                     }
                     proxy_fence();
-                    warp_arrive(smem_u32(&full[st]));
+                    warp_arrive(full_of(n));
                 }
             }
         };
@@ -1057,19 +1145,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                         }
                     }
                     if (i < halves) {      // scores of half i
-                        const uint32_t u = n + (i >> 1) * step + narrow * t, st = u % kKvStages;
-                        if (!wait(&sh.k_full[st], (u / kKvStages) & 1)) break;
+                        const uint32_t u = n + (i >> 1) * step + narrow * t, st = LO ? b : u % kKvStages;
+                        if (!wait(&sh.k_full[LO ? 2 * b + (u & 1) : st], (u / 2) & 1)) break;
                         tc_fence_after();
-                        const uint32_t k = __shfl_sync(kFull, desc_lo(kb0 + st * kOpBytes + b * (kHalf * 128), 16), 0);
+                        const uint32_t k = __shfl_sync(kFull, desc_lo(kb0 + st * kOpBytes + (LO ? 0 : b * (kHalf * 128)), 16), 0);
                         const uint32_t d = __shfl_sync(kFull, d_s + b * kHalf, 0);
                         if (elect_one()) {
 #pragma unroll
                             for (uint32_t c = 0; c < kD / 16; ++c) {
                                 const uint32_t off = (c >> 2) * ((kRows * 128) >> 4) + (c & 3) * 2;
-                                mma_ss(d, q + off, k + off, kIdescQK, c > 0);
+                                const uint32_t koff = (c >> 2) * (KeyStage<LO>::kBlock >> 4) + (c & 3) * 2;
+                                mma_ss(d, q + off, k + koff, kIdescQK, c > 0);
+                                if constexpr (LO) mma_ss(d, q + off, k + koff + (KeyStage<LO>::kRest >> 4), kIdescQK, 1);
                             }
                             tc_commit(smem_u32(&sh.s_full[2 * t + b]));
-                            if (b) {
+                            if (LO || b) {
                                 tc_commit(smem_u32(&sh.k_empty[st]));
                                 if (narrow) tc_commit(smem_u32(&sh.k_empty[st]));
                             }
