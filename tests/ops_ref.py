@@ -84,19 +84,23 @@ def evict(cfg, weights, L, keep, sink, recent):
     return kept, gone, out, len(gone) * cfg.group
 
 
-# Bounds of chunk attention. A dequantized key is rounded to f16 (2^-11 of it), so a score is off by
-# at most 2^-11 of scale * sum_d |q_d k_d| (fp32 steps: 2^-18 of it, as above), its weight by as much and the
-# normalised weight by twice that; probabilities and dequantized values add 2^-11 each, the
+# Bounds of chunk attention. A packed key is rounded by key_step of its group's largest level (one f16
+# number with bf16 storage: 2^-11; two f16 parts with fp16 storage: 2^-16, see KEY_STEP), so a score
+# is off by at most that of A = scale * sum_d |q_d| (|c s| + |z|) (fp32 steps: 2^-18 of it, as above), its weight by as
+# much and the normalised weight by twice that; probabilities and dequantized values add 2^-11 each, the
 # fp32 steps 2^-12, and the output is rounded once to its type. Errors of different tokens and
 # channels are independent, so in the 2-norm each factor counts by its root mean square: a
 # rounding of half step h has rms h / sqrt(3).
-def chunk_bounds(q, k, v, p, want, scale, half_step):
-    """(bound per output element, bound of the relative 2-norm of the whole output)."""
+KEY_STEP = {oracle.F16: 2.0 ** -16, oracle.BF16: 2.0 ** -11}
+
+
+def chunk_bounds(q, k, v, p, want, scale, half_step, key_step, kmag):
+    """(bound per output element, bound of the relative 2-norm of the whole output); kmag: |c s| + |z| of each key."""
     g = q.shape[1] // k.shape[0]
-    kh, vh = np.repeat(k, g, 0), np.repeat(v, g, 0)
+    kh, vh = np.repeat(kmag, g, 0), np.repeat(v, g, 0)
     h = 2.0 ** -11
-    a = scale * np.einsum("nhd,htd->nht", np.abs(q), np.abs(kh)).max(-1, initial=0.0)[..., None]
-    el = (2 * h * a + 2 * h + 2.0 ** -12) * np.einsum("nht,htd->nhd", p, np.abs(vh)) + half_step * np.abs(want) + 1e-7
-    rms = scale * np.sqrt(np.einsum("nhd,htd->nht", q * q, kh * kh)).max(-1, initial=0.0)
-    rel = np.sqrt((2 * (2 * rms.max(initial=0.0) ** 2 + 2) * h * h + half_step ** 2) / 3)
+    a = scale * np.einsum("nhd,htd->nht", np.abs(q), kh).max(-1, initial=0.0)[..., None]
+    el = (2 * (key_step + 2.0 ** -18) * a + 2 * h + 2.0 ** -12) * np.einsum("nht,htd->nhd", p, np.abs(vh)) + half_step * np.abs(want) + 1e-7
+    rms = key_step * scale * np.sqrt(np.einsum("nhd,htd->nht", q * q, kh * kh)).max(-1, initial=0.0)
+    rel = np.sqrt((2 * (2 * rms.max(initial=0.0) ** 2 + 2 * h * h) + half_step ** 2) / 3) + 2.0 ** -12
     return el, 2 * rel

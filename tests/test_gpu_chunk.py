@@ -7,8 +7,8 @@ import torch
 import bit_asymmetric_kv_kivi_gb300 as kivi
 import oracle
 import synth
-from gpu_util import TORCH_DT, dev_tensor, host_bits
-from ops_ref import attend, chunk_bounds, dense, visible, widen
+from gpu_util import configs, dev_tensor
+from ops_ref import KEY_STEP, attend, chunk_bounds, dense, visible, widen
 from test_gpu_window import build
 
 pytestmark = pytest.mark.gpu
@@ -24,7 +24,7 @@ def chunk_inputs(wl, new, seed=0):
     return q, [x for x, _ in kv], [x for _, x in kv]
 
 
-def check(wl, refs, q, k, v, outs, window, sinks):
+def check(wl, refs, q, k, v, outs, window, sinks, key_step=None):
     dt = refs[0].cfg.dtype
     num = den = lim = 0.0
     for b, r in enumerate(refs):
@@ -32,11 +32,12 @@ def check(wl, refs, q, k, v, outs, window, sinks):
         if n == 0:
             continue
         qf = widen(q[b], dt)
-        kc, vc, _, _ = dense(r)
+        kc, vc, km, _ = dense(r)
         kk, vv = np.concatenate([kc, widen(k[b], dt)], 1), np.concatenate([vc, widen(v[b], dt)], 1)
+        km = np.concatenate([km, np.abs(widen(k[b], dt))], 1)
         want, p = attend(qf, kk, vv, visible(r.L + n, n, window, sinks), wl.softmax_scale)
         got = outs[b].double().cpu().numpy()
-        el, rel = chunk_bounds(qf, kk, vv, p, want, wl.softmax_scale, HALF[wl.dtype])
+        el, rel = chunk_bounds(qf, kk, vv, p, want, wl.softmax_scale, HALF[wl.dtype], key_step or KEY_STEP[dt], km)
         bad = ~(np.abs(got - want) <= el)
         assert not bad.any(), (b, r.L, n, np.argwhere(bad)[:4], np.abs(got - want).max(), el.max())
         num, den, lim = num + ((got - want) ** 2).sum(), den + (want ** 2).sum(), max(lim, rel)
@@ -89,21 +90,53 @@ def test_large_scores_and_scales():
     wl = synth.Workload("scores", 2, 4, 1, 128, (300, 20), "bf16", seed=3)
     cache, refs = build(wl, 2, 2, 32, 128, 512)
     q, k, v = chunk_inputs(wl, (150, 9))
-    f = [widen(x, oracle.BF16) for x in q]
+    fq = [widen(x, oracle.BF16) for x in q]
     for s in (2.0 ** 12, 2.0 ** -30):
-        qs = [synth.to_dtype_bits(x * s, "bf16") for x in f]
+        qs = [synth.to_dtype_bits(x * s, "bf16") for x in fq]
         w = wl
         for scale in (w.softmax_scale / s, -w.softmax_scale / s, 0.0, 3 * w.softmax_scale / s):
             d = lambda xs: [dev_tensor(x, "bf16") for x in xs]   # noqa: E731
             outs = cache.chunk(d(qs), d(k), d(v), softmax_scale=scale)
             for b, r in enumerate(refs):
                 qf = widen(qs[b], oracle.BF16)
-                kc, vc, _, _ = dense(r)
-                kk, vv = (np.concatenate([c, widen(x[b], oracle.BF16)], 1) for c, x in ((kc, k), (vc, v)))
+                kc, vc, km, _ = dense(r)
+                kk, vv, km = (np.concatenate([c, f(widen(x[b], oracle.BF16))], 1)
+                              for c, x, f in ((kc, k, lambda y: y), (vc, v, lambda y: y), (km, k, np.abs)))
                 n = qf.shape[0]
                 want, p = attend(qf, kk, vv, visible(r.L + n, n, 0, 0), scale)
-                el, _ = chunk_bounds(qf, kk, vv, p, want, abs(scale), HALF["bf16"])
+                el, _ = chunk_bounds(qf, kk, vv, p, want, abs(scale), HALF["bf16"], KEY_STEP[oracle.BF16], km)
                 assert (np.abs(outs[b].double().cpu().numpy() - want) <= el).all()
+
+
+@pytest.mark.parametrize("kb", [2, 4])
+@pytest.mark.parametrize("size,key_step", [(2.0 ** -16, 2.0 ** -11), (2.0 ** -9, None), (200.0, 2.0 ** -11)])
+def test_key_magnitudes(kb, size, key_step):
+    """fp16 keys of every size: tiny ones (whose scales are subnormal f16 numbers, so the rests are too), small
+    ones, and ones past 2^13, which are kept in one f16 number."""
+    wl = synth.Workload("mags", 1, 4, 1, 128, (600,), "f16", seed=kb)
+    k0, v0 = wl.kv_seq(0, 0, 640)
+    k0 = synth.to_dtype_bits(widen(k0, oracle.F16) * size, "f16")
+    kcfg, ocfg = configs(2, "f16", 4, 1, kb=kb, vb=2)
+    cache, r = kivi.KVCache(kcfg, 1, 640), oracle.SeqCache(ocfg, 640)
+    assert r.append(np.ascontiguousarray(k0[:, :600]), np.ascontiguousarray(v0[:, :600])) == oracle.OK
+    d = lambda x: dev_tensor(np.ascontiguousarray(x), "f16")   # noqa: E731
+    cache.append([d(k0[:, :600])], [d(v0[:, :600])])
+    rng = np.random.default_rng(1)
+    q = [synth.to_dtype_bits(rng.standard_normal((40, 4, 128)), "f16")]
+    k, v = [np.ascontiguousarray(k0[:, 600:])], [np.ascontiguousarray(v0[:, 600:])]
+    scale = wl.softmax_scale / size
+    outs = cache.chunk([d(q[0])], [d(k[0])], [d(v[0])], softmax_scale=scale)
+    assert int(cache.status.item()) == 0
+    qf = widen(q[0], oracle.F16)
+    kc, vc, km, _ = dense(r)
+    kk, vv = np.concatenate([kc, widen(k[0], oracle.F16)], 1), np.concatenate([vc, widen(v[0], oracle.F16)], 1)
+    km = np.concatenate([km, np.abs(widen(k[0], oracle.F16))], 1)
+    want, p = attend(qf, kk, vv, visible(640, 40, 0, 0), scale)
+    el, rel = chunk_bounds(qf, kk, vv, p, want, scale, HALF["f16"], key_step or KEY_STEP[oracle.F16], km)
+    # levels below 2^-14 are rounded at 2^-24 of one, whatever their size
+    el = el + 2 * scale * 2.0 ** -24 * np.abs(qf).sum(-1, keepdims=True) * np.einsum("nht,htd->nhd", p, np.repeat(np.abs(vv), 4, 0))
+    got = outs[0].double().cpu().numpy()
+    assert (np.abs(got - want) <= el).all(), (np.abs(got - want) / el).max()
 
 
 def test_rows_between_sequences_and_bad_lengths():
