@@ -11,6 +11,11 @@
 // kept ones by a radix select on the weights and closes the ranks of the weights and, in a
 // paged cache, of the block table; evict_move_kernel moves a contiguous cache's groups and
 // turns the residual rings, whose slots follow the positions.
+//
+// Measured (GB300, 64 sequences of 32768 tokens, 32 query heads on 8 kv heads): the weights add 15 us to
+// an attention of 580 (16.8 MB of statistics against 1.64 GB of cache); cutting all 64 from 1020 to 512
+// groups takes 28 us: 10 to select (latency of dependent passes, about the same for one short sequence) and 18 to
+// turn 84 MB of rings (4.7 TB/s with the write).
 #include "kivi_internal.cuh"
 
 namespace kivi {

@@ -379,8 +379,9 @@ size_t kivi_decode_weights_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int3
  *   scratch_dev, scratch_bytes  at least kivi_chunk_scratch_bytes(), of any contents; calls that share it
  *               must not overlap
  *   status_dev  one int32 (may be NULL)
- * The products run on the tensor cores in f16 with fp32 accumulation: dequantized tokens and
- * probabilities are rounded to f16 (2^-11 relative). Domain: finite q with |softmax_scale * q| <= 2^100; finite k_new,
+ * The products run on the tensor cores in f16 with fp32 accumulation: dequantized values, probabilities and,
+ * with bf16 storage, dequantized keys are rounded to f16 (2^-11 relative); with fp16 storage dequantized keys
+ * below 2^13 keep 2^-16. Domain: finite q with |softmax_scale * q| <= 2^100; finite k_new,
  * v_new with magnitudes up to 65504 (the codec's domain), also in rows that no query sees.
  * Device error KIVI_ERR_LENGTH: n_new_b outside [0, max_new] (nothing is written for b), or kv_len_b outside [0,
  * max_kv_len] or more tokens than the sequence can hold (its output rows are NaN).
