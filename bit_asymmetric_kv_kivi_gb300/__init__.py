@@ -153,6 +153,14 @@ def _require(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: torc
         raise ValueError(f"{name} must be 16-byte aligned")
 
 
+def _i32(x, name: str) -> int:
+    """x as the C int32 it will be (ctypes would keep its low bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -471,13 +479,13 @@ class KVCache:
     def _decode_args(self, q, out, softmax_scale, max_kv_len):
         cfg = self.cfg
         shape = (self.nseq, cfg.num_q_heads, cfg.head_dim)
-        _require(q, "q", shape, cfg.torch_dtype, self.device)
+        _require(q, "q", shape, cfg.torch_dtype, self.kv_len.device)
         if out is None:
             out = torch.empty(shape, dtype=torch.float32, device=q.device)
         else:
-            _require(out, "out", shape, torch.float32, self.device)
+            _require(out, "out", shape, torch.float32, self.kv_len.device)
         scale = 1.0 / cfg.head_dim ** 0.5 if softmax_scale is None else softmax_scale
-        return out, float(scale), int(self.max_len if max_kv_len is None else max_kv_len)
+        return out, float(scale), _i32(self.max_len if max_kv_len is None else max_kv_len, "max_kv_len")
 
     def decode_window(self, q: torch.Tensor, window: int, sinks: int = 0, out: torch.Tensor | None = None,
                       softmax_scale: float | None = None, max_kv_len: int | None = None) -> torch.Tensor:
@@ -488,7 +496,7 @@ class KVCache:
         with _on(q.device):
             ws = self._zeroed(self._bytes(cfg.decode_ext_workspace_bytes, self.nseq, mkl))
             _check(lib().kivi_decode_window_attn(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(q),
-                                                 _ptr(out), scale, int(window), int(sinks), mkl, _ptr(ws), ws.numel(),
+                                                 _ptr(out), scale, _i32(window, "window"), _i32(sinks, "sinks"), mkl, _ptr(ws), ws.numel(),
                                                  _ptr(self.status), _stream(q.device)), "kivi_decode_window_attn")
         return out
 
@@ -510,9 +518,9 @@ class KVCache:
         if given.dim() != 2:
             raise ValueError("weights must be [nseq][groups]")
         weights_out, stride = given, int(given.shape[1])
-        _require(weights_out, "weights_out", (self.nseq, stride), torch.float32, self.device)
+        _require(weights_out, "weights_out", (self.nseq, stride), torch.float32, self.kv_len.device)
         if weights_in is not None:
-            _require(weights_in, "weights_in", (self.nseq, stride), torch.float32, self.device)
+            _require(weights_in, "weights_in", (self.nseq, stride), torch.float32, self.kv_len.device)
         with _on(q.device):
             ws = self._zeroed(self._bytes(cfg.decode_ext_workspace_bytes, self.nseq, mkl))
             sc = self._any(self._bytes(cfg.decode_weights_scratch_bytes, self.nseq, mkl))
@@ -531,7 +539,7 @@ class KVCache:
         cfg = self.cfg
         if q.dim() != 3:
             raise ValueError("q must be [rows][Hq][D]")
-        _require(q, "q", (q.shape[0], cfg.num_q_heads, cfg.head_dim), cfg.torch_dtype, self.device)
+        _require(q, "q", (q.shape[0], cfg.num_q_heads, cfg.head_dim), cfg.torch_dtype, self.kv_len.device)
         for name, t, dt in (("q_start", q_start, torch.int32), ("k_ptrs", k_ptrs, torch.int64),
                             ("v_ptrs", v_ptrs, torch.int64), ("n_new", n_new, torch.int32)):
             _require(t, name, (self.nseq,), dt, q.device)
@@ -540,18 +548,20 @@ class KVCache:
         else:
             _require(out, "out", q.shape, cfg.torch_dtype, q.device)
         scale = 1.0 / cfg.head_dim ** 0.5 if softmax_scale is None else softmax_scale
-        mkl = int(self.max_len if max_kv_len is None else max_kv_len)
+        mkl = _i32(self.max_len if max_kv_len is None else max_kv_len, "max_kv_len")
+        max_new = _i32(max_new, "max_new")
         with _on(q.device):
-            sc = self._any(self._bytes(cfg.chunk_scratch_bytes, self.nseq, int(max_new)))
+            sc = self._any(self._bytes(cfg.chunk_scratch_bytes, self.nseq, max_new))
             _check(lib().kivi_chunk_attn(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(k_ptrs),
-                                         _ptr(v_ptrs), _ptr(n_new), int(max_new), _ptr(q), _ptr(q_start), _ptr(out),
-                                         float(scale), int(window), int(sinks), mkl, _ptr(sc), sc.numel(),
+                                         _ptr(v_ptrs), _ptr(n_new), max_new, _ptr(q), _ptr(q_start), _ptr(out),
+                                         float(scale), _i32(window, "window"), _i32(sinks, "sinks"), mkl, _ptr(sc), sc.numel(),
                                          _ptr(self.status), _stream(q.device)), "kivi_chunk_attn")
         return out
 
     def chunk(self, q, k_new, v_new, window: int = 0, sinks: int = 0, softmax_scale: float | None = None):
         """chunk_attn on lists: per sequence q [n_b][Hq][D], k_new and v_new [Hkv][n_b][D] -> a list of
-        outputs like q. (Tables of pointers are made and copied per call; chunk_attn takes them as given.)"""
+        outputs like q. (Tables of pointers are made and copied per call, which a stream capture
+        does not allow; chunk_attn takes them as given.)"""
         q, k_new, v_new = list(q), list(k_new), list(v_new)
         cfg = self.cfg
         if not len(q) == len(k_new) == len(v_new) == self.nseq:
@@ -560,7 +570,7 @@ class KVCache:
         for m, k, v in zip(n, k_new, v_new):
             for t in (k, v):
                 if m:
-                    _require(t, "k_new and v_new", (cfg.num_kv_heads, m, cfg.head_dim), cfg.torch_dtype, self.device)
+                    _require(t, "k_new and v_new", (cfg.num_kv_heads, m, cfg.head_dim), cfg.torch_dtype, self.kv_len.device)
         dev = self.kv_len.device
         start = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
         kp = torch.tensor([k.data_ptr() if m else 0 for m, k in zip(n, k_new)], dtype=torch.int64).to(dev)
@@ -578,14 +588,16 @@ class KVCache:
         if weights.dim() != 2:
             raise ValueError("weights must be [nseq][groups]")
         stride = int(weights.shape[1])
-        _require(weights, "weights", (self.nseq, stride), torch.float32, self.device)
+        _require(weights, "weights", (self.nseq, stride), torch.float32, self.kv_len.device)
         if stride * cfg.group < self.max_len:
             raise ValueError(f"weights must have a column for each of {-(-self.max_len // cfg.group)} groups")
+        keep_groups = _i32(keep_groups, "keep_groups")
         with _on(weights.device):
             sc = self._any(self._bytes(_evict_scratch_bytes, self.nseq, stride))
             _check(lib().kivi_evict_groups(self._c, self.nseq, _ptr(self.seqs), _ptr(self.kv_len), _ptr(weights),
-                                           stride, int(keep_groups), int(sink_groups), int(recent_groups), _ptr(sc),
-                                           sc.numel(), _ptr(self.status), _stream(weights.device)), "kivi_evict_groups")
+                                           stride, keep_groups, _i32(sink_groups, "sink_groups"),
+                                           _i32(recent_groups, "recent_groups"), _ptr(sc), sc.numel(), _ptr(self.status),
+                                           _stream(weights.device)), "kivi_evict_groups")
         self.max_len = min(self.max_len, keep_groups * cfg.group + cfg.ring - 1)
 
     # -------------------------------------------------------------- inspection

@@ -405,7 +405,8 @@ size_t kivi_chunk_scratch_bytes(const kivi_cfg* cfg, int32_t nseq, int32_t max_n
  *   seqs_dev     contiguous sequences: the packed buffers are closed up in place. Paged ones: the
  *                block table is permuted in place (it has to be writable): the kept groups' pages
  *                first, then the dropped groups' pages, which the next groups to be packed
- *                will overwrite; entries from the old packed count on are untouched.
+ *                will overwrite; entries from the old packed count on are untouched. Where sequences share
+ *                pages, the caller replaces the shared ones among the dropped before it appends again.
  *   kv_len_dev   in/out: less m G for a sequence that lost m groups; its residual rings are turned
  *                by m G slots (slots follow positions), whole rows of unspecified contents included
  *   weights_dev  [nseq][weights_stride] fp32, in/out: closed up the same way, the weights of groups that

@@ -159,6 +159,11 @@ def test_cache_over_given_buffers():
         other.decode_window(q.bfloat16(), 300)
     with pytest.raises(ValueError):
         other.decode_weights(q, w.double())
+    for call in (lambda x: other.decode_window(q, x), lambda x: other.decode_window(q, 5, x), lambda x: other.evict(w, x),
+                 lambda x: other.evict(w, 5, x), lambda x: other.decode_window(q, 5, max_kv_len=x)):
+        for x in (2 ** 32 + 5, -2 ** 31 - 1):
+            with pytest.raises(ValueError):
+                call(x)
 
 
 def test_evict_refusals_leave_the_cache_alone():
