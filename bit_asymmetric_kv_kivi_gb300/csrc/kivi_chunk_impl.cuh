@@ -334,7 +334,8 @@ constexpr int kSegReaders = 19;           // every warp but the walking one
 
 struct ChunkShared {
     uint64_t k_full[2 * kKvStages], k_empty[kKvStages], v_full[kKvStages], v_empty[kKvStages];
-    uint64_t q_full[2], s_full[4], p_full[4], o_step[4];   // all but the first: [softmax warpgroup][half]
+    uint64_t s_full[4], p_full[4], o_step[4];   // [softmax warpgroup][half]
+    uint64_t q_full[2 * kSegs];                 // [segment slot][softmax warpgroup]
     uint64_t raw_full[kRawMax], raw_empty[kRawMax], hand_full, hand_empty, seg_full[kSegs], seg_empty[kSegs];
     ChunkSeg seg[kSegs];
     float hand_m[kRows], hand_l[kRows];   // state of the second softmax warpgroup at the end of a narrow segment
@@ -610,7 +611,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             mbar_init(smem_u32(&sh.v_empty[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.q_full[i]), 4);
             mbar_init(smem_u32(&sh.s_full[2 * i]), 1);
             mbar_init(smem_u32(&sh.s_full[2 * i + 1]), 1);
             mbar_init(smem_u32(&sh.p_full[2 * i]), 4);
@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             mbar_init(smem_u32(&sh.raw_empty[i]), 4);   // the warps that read a subtile
         }
         for (int i = 0; i < kSegs; ++i) {
+            mbar_init(smem_u32(&sh.q_full[2 * i]), 4);
+            mbar_init(smem_u32(&sh.q_full[2 * i + 1]), 4);
             mbar_init(smem_u32(&sh.seg_full[i]), 1);
             mbar_init(smem_u32(&sh.seg_empty[i]), kSegReaders);
         }
@@ -776,10 +778,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                         *reinterpret_cast<uint4*>(qt + op_addr(rk, chunk)) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
                 }
-                if (wg == tile) {
-                    proxy_fence();
-                    warp_arrive(smem_u32(&sh.q_full[tile]));
-                }
+                // (both warpgroups arrive, in narrow segments too: each is done with the segment before)
+                if (wg == tile) proxy_fence();
+                warp_arrive(smem_u32(&sh.q_full[2 * (si % kSegs) + wg]));
                 __syncwarp();
                 if (a.scale_log2 != 0.0f) sl = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 + e_mine) << 23);
             }
@@ -1113,7 +1114,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             // (The tensor core takes few products ahead, so a single issuing warp left it idle while it waited.) The
             // whole warp walks, one lane issues.
             const uint32_t t = warp == 16 ? 0 : 1;
-            uint32_t n = 0, np = 0, nq = 0;   // key tiles, probability tiles, segments so far
+            uint32_t n = 0, np = 0;   // key tiles and this warpgroup's probability tiles so far
             const uint32_t kb0 = smem_u32(sk_tile), vb0 = smem_u32(sv_tile), qb0 = smem_u32(sq_tile);
             const uint32_t d_s = __shfl_sync(kFull, tmem + t * kKeys, 0), d_o = __shfl_sync(kFull, tmem + 2 * kKeys + t * kD, 0);
             auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -1126,10 +1127,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                 // S is free for the next scores after the products of the tile before.
                 const ChunkSeg& s = sh.seg[si % kSegs];
                 const uint32_t narrow = s.it.rows <= kRows, cnt = s.x1 - s.x0, step = 1 + narrow;
-                // (both warps follow the first query tile's barrier: it completes once a segment, after
-                // everything of the segment before)
-                if (!wait(&sh.q_full[0], si & 1)) break;
-                if (!narrow && t != 0 && !wait(&sh.q_full[1], nq++ & 1)) break;
+                // (Both warps wait for both warpgroups, in narrow segments too: then every key and value tile before is
+                // done with, which the parities of their barriers rest on. A barrier for each slot of the ring, whose
+                // slots are used again once every warp is done with them, so nobody can be two phases behind.)
+                if (!wait(&sh.q_full[2 * (si % kSegs)], (si / kSegs) & 1)) break;
+                if (!wait(&sh.q_full[2 * (si % kSegs) + 1], (si / kSegs) & 1)) break;
                 const uint32_t q = __shfl_sync(kFull, desc_lo(qb0 + (narrow ? 0 : t) * kOpBytes, 16), 0);
                 // halves of this warpgroup's tiles: half i is half i & 1 of its tile i >> 1, tile (i >> 1) step + narrow t
                 // of the segment; scores run two halves ahead
