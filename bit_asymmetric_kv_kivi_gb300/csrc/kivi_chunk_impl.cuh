@@ -24,7 +24,7 @@
 // in two f16 parts (split_grid) and the scores are two products. One part puts the scores of keys with
 // outlier channels off by up to 2^-12 of their products: measured against 64 bits over 1000 to 32768
 // tokens, outputs were 6e-4 to 1.1e-3 off (2-norm), where one rounding to fp16 is 2.1e-4 and one to
-// bf16 1.7e-3; two parts give 3e-4 at fp16, and at bf16 would take 1373 us instead of 990 (2048 tokens
+// bf16 1.7e-3; two parts give 3e-4 at fp16, and at bf16 would take 1373 us instead of 995 (2048 tokens
 // over 32768) to bring 2.1e-3 - 2.6e-3 down to 1.7e-3. Stored bf16 tokens with |x| <= 65504 are
 // exact in f16 down to 2^-14 (finer ones are rounded at 2^-24). Queries are scaled per row
 // by a power of two into (1/2, 1], and the scale is applied to the fp32 scores. Probabilities are
@@ -39,11 +39,11 @@
 // tiles it sees plus an overhead; CTA c takes units [c U / C, (c + 1) U / C). A row tile that
 // several CTAs share leaves fp32 records (acc, max, sum) that chunk_merge_kernel joins.
 //
-// Measured (GB300, 2-bit, 32 query heads on 8 kv heads, bf16): 2048 tokens over 32768 990 us, 1.14
+// Measured (GB300, 2-bit, 32 query heads on 8 kv heads, bf16): 2048 tokens over 32768 995 us, 1.14
 // PFLOP/s, 60 % of what cuBLAS reaches; the TMEM pipe is busy 57 % and the issue slots 60 % of the
 // time. Bound by the handoffs of a half tile (scores, softmax, products) together with the issue slots that
 // unpacking takes: 450 us with the barriers alone, 783 with the products too, 805 with all but the
-// softmax, 886 with all but the unpack. 4 tokens over 64 x 32768: 1.40 ms, 1.17 TB/s; there each tile has 16
+// softmax, 886 with all but the unpack. 4 tokens over 64 x 32768: 1.43 ms, 1.14 TB/s; there each tile has 16
 // rows, and unpacking it (913 us by itself, eight warps that wait on each other's latencies) is what counts.
 #pragma once
 #include <type_traits>
@@ -1068,9 +1068,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
                     if (2 * half < packed) {
                         const bool wrap = raw0 + half >= Raw::kStages;
                         const uint32_t slot = wrap ? raw0 + half - Raw::kStages : raw0 + half;
-                        ok = warp_wait(smem_u32(&sh.raw_full[slot]), raw_par ^ wrap, stop);
-                        if (!ok) break;
+                        // the operand stage first: that it is free says that the tile before the last is done with, so
+                        // the raw stage's use before this one is over and its parity tells (a warp whose half had no
+                        // packed tokens for some tiles has not followed the stage's phases)
                         wait_empty();
+                        if (!ok) break;
+                        ok = warp_wait(smem_u32(&sh.raw_full[slot]), raw_par ^ wrap, stop);
                         if (!ok) break;
                         const unsigned char* from = raw_ring + slot * Raw::kBytes;
                         const int subs = packed - 2 * half < 2 ? 1 : 2;

@@ -75,6 +75,25 @@ def test_ragged_batch(g, kb, vb, G, R, dtype, paged, window, sinks):
     check(wl, refs, q, k, v, run(cache, wl, q, k, v, window, sinks), window, sinks)
 
 
+@pytest.mark.parametrize("kb,vb,dtype", [(4, 4, "f16"), (4, 4, "bf16"), (2, 2, "f16"), (2, 4, "bf16")])
+def test_many_short_sequences(kb, vb, dtype):
+    """Hundreds of segments a CTA of every kind behind one another: narrow and wide, one tile and several,
+    no packed tokens, one subtile of them, or many. Twice, bit for bit."""
+    rng = np.random.default_rng(kb + vb)
+    nseq, H, g, R = 700, 2, 4, 32
+    lengths = tuple(int(x) for x in rng.choice([0, 5, 64, 70, 96, 130, 200, 300], nseq))
+    new = [int(x) for x in rng.choice([0, 1, 2, 3, 33, 40], nseq, p=[0.1, 0.3, 0.2, 0.2, 0.1, 0.1])]
+    wl = synth.Workload("short", nseq, g * H, H, 128, lengths, dtype, seed=19)
+    cache, refs = build(wl, kb, vb, 32, R, 320, paged=True)
+    q, k, v = chunk_inputs(wl, new, 5)
+    outs = run(cache, wl, q, k, v)
+    check(wl, refs, q, k, v, outs, 0, 0)
+    for _ in range(3):
+        again = run(cache, wl, q, k, v)
+        assert all(torch.equal(a, b) for a, b in zip(outs, again))
+    check(wl, refs, q, k, v, run(cache, wl, q, k, v, 60, 10), 60, 10)
+
+
 @pytest.mark.parametrize("H,g,n", [(1, 4, 3), (2, 1, 1), (1, 8, 64)])
 def test_long_cache_split_over_ctas(H, g, n):
     """Few rows over a long cache: every CTA takes a part and the parts are joined."""
