@@ -355,6 +355,7 @@ class KVCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.max_len = max_len      # host upper bound on every kv_len
         self._ws = None
+        self._ext_ws = None
         self._scratch = None
         self._old = []
         self._sizes = {}
@@ -467,9 +468,11 @@ class KVCache:
         return n
 
     def _zeroed(self, need: int) -> torch.Tensor:
-        """The workspace that every attention call leaves zero-filled, at least `need` bytes."""
-        self._ws = self._grown(self._ws, need, torch.zeros)
-        return self._ws
+        """The workspace that windows and weights leave zero-filled, at least `need` bytes. Not the one of
+        `workspace`: that one is replaced when decode or decode_multi need more, under a graph that names
+        it, and made inside a capture it is filled at replay only."""
+        self._ext_ws = self._grown(self._ext_ws, need, torch.zeros)
+        return self._ext_ws
 
     def _any(self, need: int) -> torch.Tensor:
         """Scratch of any contents, at least `need` bytes."""

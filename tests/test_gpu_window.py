@@ -68,7 +68,7 @@ def test_window_edges(g, kb, vb, G, R, dtype, window, sinks):
     cache, refs = build(wl, kb, vb, G, R, 2560, paged=g % 2 == 1)
     out = cache.decode_window(dev_tensor(wl.query(0), dtype), window, sinks, softmax_scale=wl.softmax_scale)
     check(wl, cache, refs, out, window, sinks)
-    assert int(cache._ws.count_nonzero()) == 0
+    assert int(cache._ext_ws.count_nonzero()) == 0
 
 
 def test_window_long_stream_precision():
@@ -122,7 +122,7 @@ def test_weights(g, kb, vb, G, R, dtype, decay):
     check(wl, cache, refs, out, 0, 0, got.cpu().numpy(), before, decay)
     again, got2 = cache.decode_weights(q, w_in, None, decay=decay, softmax_scale=wl.softmax_scale)   # in place
     assert got2 is w_in and torch.equal(got2, got) and torch.equal(again, out)
-    assert int(cache._ws.count_nonzero()) == 0
+    assert int(cache._ext_ws.count_nonzero()) == 0
     _, got3 = cache.decode_weights(q, None, softmax_scale=wl.softmax_scale)
     assert got3.shape == (wl.batch, cache.weight_groups())
 
@@ -159,3 +159,31 @@ def test_window_and_weights_captured_and_replayed():
         torch.cuda.synchronize()
         check(wl, cache, refs, out, 256, 4)
         assert abs(float(w.sum()) - 3 * 8) < 1e-3
+
+
+def test_captured_window_beside_decode_that_grows_its_workspace():
+    """A graph's workspace stays its own when decode and decode_multi make and replace theirs, inside a
+    capture and outside, and memory that they gave back is written."""
+    wl = synth.Workload("beside", 3, 8, 2, 128, (4000, 161, 2900), "f16", seed=19)
+    cache, refs = build(wl, 2, 2, 32, 128, 4096)
+    q = dev_tensor(wl.query(0), "f16")
+    out = torch.zeros((3, 8, 128), device="cuda")
+    cache.decode(q)
+    cache._ws = None
+    other = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(other):
+        cache.decode(q)              # its workspace belongs to this graph, filled at replay
+    cache.decode_window(q, 256, 4, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.decode_window(q, 256, 4, out=out)
+    many = q[:, None].expand(3, 8, 8, 128).contiguous()
+    cache._ws = None
+    for n in (1, 8):
+        cache.decode_multi(many[:, :n].contiguous())
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 10, 1 << 16, 1 << 20, 1 << 22) * 2]
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    check(wl, cache, refs, out, 256, 4)
+    assert int(cache._ext_ws.count_nonzero()) == 0 and len(junk) == 8
