@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) chunk_kernel(ChunkArgs a) {
             const int64_t qrow = (static_cast<int64_t>(a.q_start[s.it.b]) + qi) * a.Hq + s.h * g + (row - qi * g);
             float sl = 1.0f;        // log2 units per score of this thread's row
             // This warp's 32 rows of Q, 16 lanes a row, scaled by a power of two to |q| in (1/2, 1], in K's channel
-            // order. (A lane per row took 12000 clocks a segment, this a third of it.)
+            // order. (A lane per row took 12000 .. 14000 clocks a segment, this 9000 .. 12000.)
             {
                 const int chunk = lane & 15, base = s.it.row0 + tile * kRows + (r & ~31), end = s.it.row0 + s.it.rows;
                 const int64_t q0 = static_cast<int64_t>(a.q_start[s.it.b]) * a.Hq + s.h * g;   // the first query's first head
